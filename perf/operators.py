@@ -240,13 +240,21 @@ def _group(s, c):
             torch.where(live, s["slot"].long()[token], -1).to(torch.int32))
 
 
+def _rounded(x, dtype):
+    """`x` in 64 bits, rounded once: what the step through 32 bits drops goes into their last bit."""
+    f = x.float()
+    back = f.double()
+    bits = f.view(torch.int32) - (back.abs() > x.abs()).int()
+    return torch.where(back != x, bits | 1, bits).view(torch.float32).to(dtype) if dtype != torch.float32 else f
+
+
 def _quantise_rows(s, c):
     x = s["x"]
     if s["index"] is not None:
         x = x[s["index"].long()]
     if c["silu"]:
         gate, up = x[:, :c["F"]].double(), x[:, c["F"]:].double()  # it is rounded next to its borders
-        x = (gate / (1 + (-gate).exp()) * up).to(x.dtype)
+        x = _rounded(gate / (1 + (-gate).exp()) * up, x.dtype)
     return x if s["rows_out"] is not None else None, _values(*_quantise(x)).to(torch.bfloat16)
 
 
@@ -388,7 +396,11 @@ def exact(case, seed):
         x = x[s["index"].long()] if s["index"] is not None else x
         if c["silu"]:
             x = x[:, :c["F"]] * torch.sigmoid(x[:, :c["F"]]) * x[:, c["F"]:]
-        held = x.to(s["x"].dtype).double()
+        held = x
+        if c["silu"]:  # rounded to the type that holds it, to the nearest of its steps
+            kept = torch.finfo(s["x"].dtype)
+            step = 2.0 ** torch.floor(torch.log2(x.abs().clamp_min(kept.smallest_normal))) * kept.eps
+            held = torch.round(x / step) * step
         return x if s["rows_out"] is not None else None, _nearest(held)
     if op == "linear":
         return _decode(s["x_codes"], s["x_scales"]) @ _decode(s["w_codes"][0], s["w_scales"][0]).T
