@@ -1,0 +1,576 @@
+// Routing of tokens to experts, the grouping of (token, choice) pairs by
+// expert, and the weighted combine of the experts' rows: what stands between
+// the router fold (lora_apply_router), the expert fold (lora_expert_apply) and
+// the layer's output.
+//
+// Sources: spark_model/lora/expert_apply.rs, module text (the router delta
+// lands before top-k; the fold works on rows sorted by expert_offsets, before
+// moe_unpermute_reduce_indexed).
+#include <mutex>
+
+#include "elem.cuh"
+#include "experts.h"
+
+namespace lora {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Ordered keys: unsigned integers that compare as the finite numbers they come
+// from (+0 and -0 alike); 0 is below all of them and marks what cannot be chosen.
+// ---------------------------------------------------------------------------
+
+LORA_DEV uint32_t order_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+LORA_DEV float value_of(uint32_t u) {
+  return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
+LORA_DEV uint64_t order_of(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+  return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
+}
+LORA_DEV double value_of(uint64_t u) {
+  return __longlong_as_double((long long)((u >> 63) ? (u & 0x7fffffffffffffffull) : ~u));
+}
+
+LORA_DEV uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+LORA_DEV uint64_t warp_max(uint64_t v) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+  const uint32_t lo =
+      __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+template <typename V>
+struct KeyOf;
+template <>
+struct KeyOf<float> { typedef uint32_t U; };
+template <>
+struct KeyOf<double> { typedef uint64_t U; };
+
+// The warp's row of logits: lane l holds experts [l * VPL, (l + 1) * VPL).
+// Experts past E, and those whose logit is -inf, NaN or +inf, come as -inf;
+// the last two set *bad.
+template <int VPL, typename LT>
+LORA_DEV void load_row(const LT* row, int lane, int E, float (&x)[VPL], bool* bad) {
+  const int e0 = lane * VPL;
+  constexpr int kBytes = VPL * (int)sizeof(LT);
+  if (E % VPL == 0 && kBytes >= 4) {
+    // the lane's share is whole or empty, and aligned to its size (or 16 bytes)
+    constexpr int kVec = kBytes >= 16 ? 16 : kBytes;
+    constexpr int kN = kBytes / kVec == 0 ? 1 : kBytes / kVec;
+    uint32_t w[kBytes < 4 ? 1 : kBytes / 4];
+    if (e0 < E) {
+      const LT* p = row + e0;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        if (kVec == 16) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+          w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        } else if (kVec == 8) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+          w[0] = v.x; w[1] = v.y;
+        } else {
+          w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        }
+      }
+      const LT* q = reinterpret_cast<const LT*>(w);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) x[i] = to_f32(q[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) x[i] = -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) x[i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (!(x[i] < INFINITY)) {   // NaN or +inf
+      x[i] = -INFINITY;
+      *bad = true;
+    }
+}
+
+// Scores s of the lane's experts and their selection keys s + bias, in V.
+// Returns the largest score of the row.
+template <int VPL, typename V>
+LORA_DEV V scores(const RouteParams& p, int lane, const float (&x)[VPL], V (&s)[VPL]) {
+  if (p.score == LORA_SCORE_SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s[i] = (V)1 / ((V)1 + exp(-(V)x[i]));
+    return (V)1;
+  }
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
+  {
+    const uint32_t u = warp_max(m > -INFINITY ? order_of(m) : 0u);
+    m = u != 0u ? value_of(u) : 0.0f;
+  }
+  V sum = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    s[i] = exp((V)x[i] - (V)m);
+    sum += s[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const V inv = (V)1 / sum;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) s[i] = s[i] * inv;
+  return inv;   // the largest: exp(0) / sum
+}
+
+// Keeps the experts of the best top_groups groups (ties to the lowest group),
+// clearing the others' keys.  Group g holds the n = E / num_groups experts from
+// g * n on; its score is its largest key, or the sum of its two largest (one
+// alone counts alone).  Lane g holds group g's score while they are compared.
+// Returns whether the border between kept and dropped is within tol(value).
+template <int VPL, typename V, typename Tol>
+LORA_DEV bool keep_groups(const RouteParams& p, int lane, typename KeyOf<V>::U (&u)[VPL],
+                          Tol tol) {
+  typedef typename KeyOf<V>::U U;
+  const int n = p.E / p.num_groups;
+  const bool pair = p.group_score == LORA_GROUP_TOP_PAIR;
+  U mine = 0;   // this lane's group's score
+  for (int g = 0; g < p.num_groups; ++g) {
+    U a = 0, b = 0;   // the lane's two largest keys in group g
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane * VPL + i;
+      const U v = (e >= g * n && e < (g + 1) * n) ? u[i] : 0;
+      b = max(b, min(a, v));
+      a = max(a, v);
+    }
+    const U top = warp_max(a);
+    U score = top;
+    if (pair && top != 0) {
+      // the second largest: the best lane's runner-up, or another lane's best
+      const uint32_t holders = __ballot_sync(0xffffffffu, a == top);
+      const bool first = lane == __ffs((int)holders) - 1;
+      const U second = warp_max(first ? b : a);
+      if (second != 0) score = order_of(value_of(top) + value_of(second));
+    }
+    if (lane == g) mine = score;
+  }
+  // rank of this lane's group among all
+  int rank = 0;
+  for (int g = 0; g < p.num_groups; ++g) {
+    const U other = __shfl_sync(0xffffffffu, mine, g);
+    rank += (other > mine || (other == mine && g < lane)) ? 1 : 0;
+  }
+  const bool kept = lane < p.num_groups && rank < p.top_groups && mine != 0;
+  const uint32_t keep = __ballot_sync(0xffffffffu, kept);
+  const U worst_kept = ~warp_max(kept ? (U)~mine : (U)0);   // smallest kept score
+  const U best_out = warp_max(lane < p.num_groups && !kept ? mine : (U)0);
+  const bool close = best_out != 0 && keep != 0 &&
+                     value_of(worst_kept) - value_of(best_out) <= tol(value_of(worst_kept));
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane * VPL + i;
+    if (e < p.E && !((keep >> (e / n)) & 1u)) u[i] = 0;
+  }
+  return close;
+}
+
+// The top_k largest keys in descending order, ties to the lowest expert: lane
+// j returns the j-th choice (-1 when nothing is left).  *close is set when two
+// neighbours in that order, or the last choice and the best one left, are
+// within tol(value) of each other (Tol::kExact: not looked at).
+template <int VPL, typename V, typename Tol>
+LORA_DEV int take_best(const RouteParams& p, int lane, typename KeyOf<V>::U (&u)[VPL], Tol tol,
+                       bool* close) {
+  typedef typename KeyOf<V>::U U;
+  U best = 0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) best = max(best, u[i]);
+  int id = -1;
+  U prev = 0;
+  const int rounds = p.top_k + (Tol::kExact ? 0 : 1);
+  for (int j = 0; j < rounds; ++j) {
+    const U m = warp_max(best);
+    if (m == 0) break;
+    if (!Tol::kExact && prev != 0 && value_of(prev) - value_of(m) <= tol(value_of(prev)))
+      *close = true;
+    prev = m;
+    if (j == p.top_k) break;
+    const int src = __ffs((int)__ballot_sync(0xffffffffu, best == m)) - 1;
+    int at = 0;
+    if (lane == src) {
+#pragma unroll
+      for (int i = VPL - 1; i >= 0; --i)
+        if (u[i] == m) at = i;
+      best = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (i == at) u[i] = 0;
+        best = max(best, u[i]);
+      }
+    }
+    at = __shfl_sync(0xffffffffu, at, src);
+    if (lane == j) id = src * VPL + at;
+  }
+  return id;
+}
+
+struct Exact {
+  static constexpr bool kExact = true;
+  template <typename V>
+  LORA_DEV V operator()(V) const { return (V)-1; }
+};
+// Twice the error of an fp32 key: the score's (expf and a division within 8
+// ulps, the softmax sum within VPL + 5 more: 2^-18 of the row's largest score)
+// and the rounding of the bias sum.  A pair's sum has twice a key's.
+struct Within {
+  static constexpr bool kExact = false;
+  float of_score;
+  LORA_DEV float operator()(float v) const { return of_score + 0x1p-21f * fabsf(v); }
+};
+
+// Selection keys s + bias of the lane's experts; experts with a masked logit or
+// bias get key 0.
+template <int VPL, typename V>
+LORA_DEV void make_keys(const RouteParams& p, int lane, const float (&x)[VPL],
+                        const V (&s)[VPL], typename KeyOf<V>::U (&u)[VPL], bool* bad) {
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane * VPL + i;
+    float b = 0.0f;
+    if (p.bias != nullptr && e < p.E) b = __ldg(p.bias + e);
+    if (!(b < INFINITY)) *bad = true;
+    u[i] = (x[i] > -INFINITY && b > -INFINITY && b < INFINITY) ? order_of(s[i] + (V)b) : 0;
+  }
+}
+
+// The same selection in 64 bits, for the tokens whose fp32 keys come too close
+// to tell apart.
+template <int VPL, typename LT>
+__device__ __noinline__ int select_in_double(const RouteParams& p, const LT* row, int lane) {
+  float x[VPL];
+  double s[VPL];
+  uint64_t u[VPL];
+  bool bad = false, close = false;
+  load_row<VPL, LT>(row, lane, p.E, x, &bad);
+  scores<VPL, double>(p, lane, x, s);
+  make_keys<VPL, double>(p, lane, x, s, u, &bad);
+  if (p.num_groups > 1) keep_groups<VPL, double>(p, lane, u, Exact());
+  return take_best<VPL, double>(p, lane, u, Exact(), &close);
+}
+
+// One warp per token.  Without a bias (and without pair scores of groups) the
+// order of the scores is the order of the logits, so the logits themselves are
+// the keys and the choice is exact.  Else the keys are fp32 scores plus bias;
+// where two that decide the outcome lie within their error bound the token is
+// done again in 64 bits (the filter), so that the chosen experts are those of
+// exact arithmetic.
+template <int VPL, typename LT>
+__global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
+  const int lane = threadIdx.x & 31;
+  const long long t = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (t >= p.T) return;
+  const LT* row = reinterpret_cast<const LT*>(p.logits) + (size_t)t * p.E;
+  float x[VPL];
+  uint32_t u[VPL];
+  bool bad = false;
+  load_row<VPL, LT>(row, lane, p.E, x, &bad);
+  const bool pair = p.num_groups > 1 && p.group_score == LORA_GROUP_TOP_PAIR;
+  const bool by_score = p.bias != nullptr || pair;
+  int id;
+  float inv_sum = 1.0f, row_max = 0.0f;   // softmax normalisation, where it is needed
+  if (by_score) {
+    float s[VPL];
+    const float smax = scores<VPL, float>(p, lane, x, s);
+    make_keys<VPL, float>(p, lane, x, s, u, &bad);
+    const Within tol = {0x1p-17f * smax};
+    bool close = false;
+    if (p.num_groups > 1) {
+      const Within tol2 = {0x1p-16f * smax};
+      close = keep_groups<VPL, float>(p, lane, u, tol2);
+    }
+    id = take_best<VPL, float>(p, lane, u, tol, &close);
+    if (close) id = select_in_double<VPL, LT>(p, row, lane);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) u[i] = x[i] > -INFINITY ? order_of(x[i]) : 0u;
+    bool close = false;
+    if (p.num_groups > 1) keep_groups<VPL, float>(p, lane, u, Exact());
+    id = take_best<VPL, float>(p, lane, u, Exact(), &close);
+  }
+  if (p.score == LORA_SCORE_SOFTMAX && !p.renormalize) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
+    const uint32_t mu = warp_max(m > -INFINITY ? order_of(m) : 0u);
+    row_max = mu != 0u ? value_of(mu) : 0.0f;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) sum += expf(x[i] - row_max);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    inv_sum = 1.0f / sum;
+  }
+  // weights: lane j has the j-th choice
+  const bool live = id >= 0;
+  const float xs = live ? to_f32(row[id]) : -INFINITY;
+  float w;
+  if (p.renormalize) {
+    // relative to the largest chosen score, so that nothing underflows to 0 / 0
+    const uint32_t mu = warp_max(live ? order_of(xs) : 0u);
+    const float top = mu != 0u ? value_of(mu) : 0.0f;
+    if (p.score == LORA_SCORE_SOFTMAX) {
+      w = live ? expf(xs - top) : 0.0f;
+    } else {
+      const float m = fminf(top, 0.0f);
+      w = !live ? 0.0f : xs >= 0.0f ? 1.0f / (1.0f + expf(-xs)) : expf(xs - m) / (1.0f + expf(xs));
+    }
+    float sum = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    w = live ? w / sum : 0.0f;
+  } else if (p.score == LORA_SCORE_SOFTMAX) {
+    w = live ? expf(xs - row_max) * inv_sum : 0.0f;
+  } else {
+    w = live ? 1.0f / (1.0f + expf(-xs)) : 0.0f;
+  }
+  if (lane < p.top_k) {
+    const size_t o = (size_t)t * p.top_k + lane;
+    p.ids[o] = id;
+    p.weights[o] = w * p.scale;
+  }
+  if (p.flags != nullptr && __any_sync(0xffffffffu, bad) && lane == 0)
+    raise_flag(p.flags, LORA_FLAG_NONFINITE);
+}
+
+template <typename LT>
+cudaError_t route_typed(const RouteParams& p, cudaStream_t stream) {
+  const int warps = 8;
+  const int threads = p.T < warps ? 32 * p.T : 32 * warps;
+  const unsigned grid = (unsigned)(((long long)p.T + warps - 1) / warps);
+  const int per_lane = (p.E + 31) / 32;
+  if (per_lane <= 1) route_kernel<1, LT><<<grid, threads, 0, stream>>>(p);
+  else if (per_lane <= 2) route_kernel<2, LT><<<grid, threads, 0, stream>>>(p);
+  else if (per_lane <= 4) route_kernel<4, LT><<<grid, threads, 0, stream>>>(p);
+  else if (per_lane <= 8) route_kernel<8, LT><<<grid, threads, 0, stream>>>(p);
+  else if (per_lane <= 16) route_kernel<16, LT><<<grid, threads, 0, stream>>>(p);
+  else route_kernel<32, LT><<<grid, threads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Grouping: a stable counting sort of the pairs by expert, in one launch of
+// one thread-block cluster.  CTA c takes the c-th run of pairs and warp w of it
+// the w-th share of that run, so (CTA, warp, position) order is pair order.
+//   1. every warp counts its pairs per expert (in its own table: no atomics);
+//   2. per expert, a prefix over the warps, then over the CTAs' totals through
+//      distributed shared memory, then over the experts;
+//   3. every warp walks its pairs again and hands out rows.
+// ---------------------------------------------------------------------------
+
+constexpr int kGrThreads = 1024;
+constexpr int kGrWarps = kGrThreads / 32;
+
+LORA_DEV int pair_expert(const GroupParams& p, int i, int end, bool* bad) {
+  int e = -1;
+  if (i < end) {
+    e = __ldg(p.ids + i);
+    if (e < -1 || e >= p.E) {
+      e = -1;
+      *bad = true;
+    }
+  }
+  return e;
+}
+
+__global__ void __launch_bounds__(kGrThreads, 1) group_kernel(const GroupParams p) {
+  extern __shared__ int gr_smem[];
+  __shared__ int scratch[kGrWarps];
+  int* total = gr_smem;             // [E]: this CTA's pairs per expert
+  int* table = gr_smem + p.E;       // [kGrWarps][E]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ctas = (int)gridDim.x, rank = (int)blockIdx.x;
+  // shares in whole warps' steps
+  const int steps = (p.n + 32 * kGrWarps * ctas - 1) / (32 * kGrWarps * ctas);
+  const long long first = ((long long)rank * kGrWarps + warp) * steps * 32;
+  const int begin = (int)min(first, (long long)p.n);
+  const int end = (int)min(first + (long long)steps * 32, (long long)p.n);
+  int* mine = table + warp * p.E;
+  for (int e = lane; e < p.E; e += 32) mine[e] = 0;
+  __syncwarp();
+  bool bad = false;
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    const int e = pair_expert(p, i0 + lane, end, &bad);
+    const uint32_t same = __match_any_sync(0xffffffffu, e);
+    if (e >= 0 && lane == __ffs((int)same) - 1) mine[e] += __popc(same);
+    __syncwarp();
+  }
+  if (p.flags != nullptr && __any_sync(0xffffffffu, bad) && lane == 0)
+    raise_flag(p.flags, LORA_FLAG_BAD_EXPERT);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kGrThreads) {
+    int run = 0;
+    for (int w = 0; w < kGrWarps; ++w) {
+      const int c = table[w * p.E + e];
+      table[w * p.E + e] = run;
+      run += c;
+    }
+    total[e] = run;
+  }
+  cluster_sync();
+  // kRouteMaxExperts == kGrThreads: one expert per thread
+  const int e = threadIdx.x;
+  int before = 0, all = 0;
+  if (e < p.E) {
+    for (int c = 0; c < ctas; ++c) {
+      const int t = dsmem_ld_s32(dsmem_addr(total + e, (uint32_t)c));
+      if (c < rank) before += t;
+      all += t;
+    }
+  }
+  int rows = 0;
+  const int incl = block_inclusive_scan<kGrThreads>(all, scratch, &rows);
+  if (e < p.E) {
+    const int base = incl - all;
+    if (rank == 0) p.expert_offsets[e] = base;
+    for (int w = 0; w < kGrWarps; ++w) table[w * p.E + e] += base + before;
+  }
+  if (rank == 0 && threadIdx.x == 0) p.expert_offsets[p.E] = rows;
+  cluster_sync();   // also: no CTA leaves while its totals are read
+  for (int i0 = begin; i0 < end; i0 += 32) {
+    const int i = i0 + lane;
+    const int ex = pair_expert(p, i, end, &bad);
+    const uint32_t same = __match_any_sync(0xffffffffu, ex);
+    int row = -1;
+    if (ex >= 0) row = mine[ex] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (ex >= 0 && lane == __ffs((int)same) - 1) mine[ex] += __popc(same);
+    __syncwarp();
+    if (i < end) {
+      p.pair_row[i] = row;
+      if (row >= 0) {
+        const int t = i / p.top_k;
+        p.row_token[row] = t;
+        if (p.row_slot != nullptr) p.row_slot[row] = __ldg(p.token_slot + t);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Combine: out[t] = residual[t] + sum_j w[t, j] y[pair_row[t, j]], fp32, in
+// order of j, rounded once.  A thread owns eight columns of one token.
+// ---------------------------------------------------------------------------
+
+template <typename T>
+__global__ void __launch_bounds__(256) combine_kernel(const CombineParams p) {
+  const int cols = p.F >> 3;
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (long long)p.T * cols) return;
+  const int t = (int)(i / cols), c = (int)(i - (long long)t * cols) * 8;
+  const T* y = reinterpret_cast<const T*>(p.y);
+  float acc[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) acc[q] = 0.0f;
+  if (p.residual != nullptr) {
+    Raw8<T> r;
+    r.load(reinterpret_cast<const T*>(p.residual) + (size_t)t * p.F + c);
+    r.get(acc);
+  }
+  bool bad = false;
+  for (int j0 = 0; j0 < p.top_k; j0 += 8) {
+    Raw8<T> v[8];
+    float w[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      int row = -1;
+      if (j0 + q < p.top_k) {
+        row = __ldg(p.pair_row + (size_t)t * p.top_k + j0 + q);
+        if (row < -1 || row >= p.rows_cap) {
+          row = -1;
+          bad = true;
+        }
+      }
+      w[q] = 0.0f;
+      if (row >= 0) {
+        w[q] = __ldg(p.weights + (size_t)t * p.top_k + j0 + q);
+        v[q].load(y + (size_t)row * p.F + c);
+      } else {
+        const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        v[q].set(zero);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      float f[8];
+      v[q].get(f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[q], f[k], acc[k]);
+    }
+  }
+  Raw8<T> o;
+  o.set(acc);
+  o.store(reinterpret_cast<T*>(p.out) + (size_t)t * p.F + c);
+  if (bad && c == 0) raise_flag(p.flags, LORA_FLAG_BAD_ROW);
+}
+
+template <typename T>
+cudaError_t combine_typed(const CombineParams& p, cudaStream_t stream) {
+  const long long n = (long long)p.T * (p.F >> 3);
+  const unsigned grid = (unsigned)((n + 255) / 256);
+  combine_kernel<T><<<grid, 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+std::mutex g_mu;
+bool g_group_attr[64];
+
+}  // namespace
+
+cudaError_t route_launch(const RouteParams& p, int type, cudaStream_t stream) {
+  if (type == LORA_TYPE_BF16) return route_typed<__nv_bfloat16>(p, stream);
+  if (type == LORA_TYPE_F16) return route_typed<__half>(p, stream);
+  return route_typed<float>(p, stream);
+}
+
+cudaError_t group_launch(const GroupParams& p, cudaStream_t stream) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_group_attr[dev]) {
+      err = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (kGrWarps + 1) * kRouteMaxExperts * 4);
+      if (err != cudaSuccess) return err;
+      g_group_attr[dev] = true;
+    }
+  }
+  // one CTA per 4096 pairs, up to a cluster of eight
+  int ctas = 1;
+  while (ctas < 8 && (long long)ctas * 4096 < p.n) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+  cfg.blockDim = dim3(kGrThreads, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)(kGrWarps + 1) * p.E * 4;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, group_kernel, p);
+}
+
+cudaError_t combine_launch(const CombineParams& p, int type, cudaStream_t stream) {
+  if (type == LORA_TYPE_BF16) return combine_typed<__nv_bfloat16>(p, stream);
+  if (type == LORA_TYPE_F16) return combine_typed<__half>(p, stream);
+  return combine_typed<float>(p, stream);
+}
+
+}  // namespace lora

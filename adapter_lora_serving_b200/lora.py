@@ -27,6 +27,9 @@ LORA_FLAG_BAD_SLOT = 8
 LORA_FLAG_BAD_PAIR = 16
 LORA_FLAG_BAD_OFFSETS = 32
 LORA_FLAG_TIMEOUT = 64
+LORA_FLAG_BAD_EXPERT = 128
+LORA_FLAG_BAD_ROW = 256
+LORA_FLAG_NONFINITE = 512
 
 LORA_REGIME_AUTO = 0
 LORA_REGIME_BGMV = 1
@@ -41,12 +44,30 @@ LORA_OP_GATHER_SHRINK = 3
 LORA_OP_APPLY_EMBEDDING = 4
 LORA_OP_EXPERT_APPLY = 5
 
+LORA_TYPE_BF16 = 0
+LORA_TYPE_F16 = 1
+LORA_TYPE_F32 = 2
+
+LORA_SCORE_SOFTMAX = 0
+LORA_SCORE_SIGMOID = 1
+
+LORA_GROUP_MAX = 0
+LORA_GROUP_TOP_PAIR = 1
+
+LORA_ACT_NONE = 0
+LORA_ACT_SILU_MUL = 1
+
+LORA_ROUTE_MAX_EXPERTS = 1024
+LORA_ROUTE_MAX_TOP_K = 32
+LORA_ROUTE_MAX_GROUPS = 32
+
 LORA_STATIC_SCRATCH_BYTES = 16 << 20
 
 # (name, restype, argtypes) of every exported symbol.
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _Z = ctypes.c_size_t
+_F = ctypes.c_float
 _SIGS = [
     ("lora_shrink", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
     ("lora_expand", _I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _I, _I, _P, _P]),
@@ -61,6 +82,14 @@ _SIGS = [
      [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _I, _P, _P]),
     ("lora_expert_apply", _I,
      [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P, _Z, _P, _P]),
+    ("lora_route_experts", _I,
+     [_P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P]),
+    ("lora_group_experts", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P]),
+    ("lora_mx_quantize", _I, [_P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    ("lora_mx_dequantize", _I, [_P, _P, _P, _I, _I, _I, _P]),
+    ("lora_mx_linear", _I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
+    ("lora_mx_expert_linear", _I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
+    ("lora_combine_experts", _I, [_P, _I, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     ("lora_workspace_bytes", _Z, [_I, _I, _I, _I, _I, _I]),
     ("lora_resolve_regime", _I, [_I, _I, _I, _I, _I]),
     ("lora_plan_tile", _I, [_I, _I]),
@@ -203,6 +232,200 @@ def lora_expert_apply(x_sorted, y_sorted, a, b, pair_index, ranks, scalings, row
                                     num_experts, slots, num_pairs, R, _slices(out_slices),
                                     len(out_slices), _ptr(workspace), workspace_bytes,
                                     _ptr(err_flags), _stream(stream)))
+
+
+# The routed layer's entry points below look at the tensors they are given: a
+# tensor's type, size, contiguity and device are checked (LORA_ERR_INVALID), its
+# element type picks `type`, and the call runs on the tensors' device and that
+# device's current stream.  Raw device pointers (ints) are passed unchecked, on
+# the current device.
+
+_types = None
+
+
+def _type_table():
+    global _types
+    if _types is None:
+        import torch
+        _types = {torch.bfloat16: LORA_TYPE_BF16, torch.float16: LORA_TYPE_F16,
+                  torch.float32: LORA_TYPE_F32, torch.int32: "int32", torch.uint8: "uint8"}
+    return _types
+
+
+def _refuse(op, what):
+    raise LoraError("LORA_ERR_INVALID", f"{op}: {what}")
+
+
+def _run(op, device_of, stream, call):
+    """`call(stream)` on the device of `device_of` (a tensor, or anything else for
+    the current device); raises on a non-OK status."""
+    if stream is not None and not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device_of is None or isinstance(device_of, int):
+        _check(call(_stream(stream)))
+        return
+    import torch
+    device = device_of.device
+    if device.index == torch.cuda.current_device():
+        _check(call(torch.cuda.current_stream().cuda_stream if stream is None else stream))
+        return
+    with torch.cuda.device(device):
+        _check(call(torch.cuda.current_stream().cuda_stream if stream is None else stream))
+
+
+def _tensors(op, *specs):
+    """Pointers of (name, tensor, kind, least number of elements) and the first
+    tensor among them.  kind: "int32", "uint8", an LORA_TYPE_*, or None (any
+    LORA_TYPE_*)."""
+    table = _types or _type_table()
+    ptrs, first = [], None
+    for name, t, kind, least in specs:
+        if t is None or isinstance(t, int):
+            ptrs.append(t)
+            continue
+        got = table.get(t.dtype)
+        if got != kind and (kind is not None or not isinstance(got, int)):
+            _refuse(op, f"{name} has element type {t.dtype}")
+        if first is None:
+            first = t
+            if not t.is_cuda:
+                _refuse(op, f"{name} is not on a CUDA device")
+        elif t.device != first.device:
+            _refuse(op, f"{name} is on {t.device}, not on {first.device}")
+        if not t.is_contiguous():
+            _refuse(op, f"{name} is not contiguous")
+        if t.numel() < least:
+            _refuse(op, f"{name} has {t.numel()} elements, fewer than {least}")
+        ptrs.append(t.data_ptr())
+    return ptrs, first
+
+
+def _type_of(op, name, t, given):
+    if given is not None:
+        return given
+    kind = (_types or _type_table()).get(getattr(t, "dtype", None))
+    if not isinstance(kind, int):
+        _refuse(op, f"{name} has no element type of LORA_TYPE_*: give `type` with a raw pointer")
+    return kind
+
+
+def lora_route_experts(logits, bias, topk_ids, topk_weights, T, num_experts, top_k,
+                       score=LORA_SCORE_SOFTMAX, num_groups=1, top_groups=1,
+                       group_score=LORA_GROUP_MAX, renormalize=True, scale=1.0, type=None,
+                       err_flags=None, stream=None):
+    """Chosen experts and their weights from routing logits (after
+    lora_apply_router)."""
+    op = "lora_route_experts"
+    kind = _type_of(op, "logits", logits, type)
+    (lp, bp, ip, wp, fp), first = _tensors(
+        op, ("logits", logits, kind, T * num_experts), ("bias", bias, LORA_TYPE_F32, num_experts),
+        ("topk_ids", topk_ids, "int32", T * top_k),
+        ("topk_weights", topk_weights, LORA_TYPE_F32, T * top_k),
+        ("err_flags", err_flags, "int32", 1))
+    fn = (_lib or load()).lora_route_experts
+    _run(op, first, stream,
+         lambda s: fn(lp, kind, bp, ip, wp, T, num_experts, top_k, score, num_groups, top_groups,
+                      group_score, 1 if renormalize else 0, scale, fp, s))
+
+
+def lora_group_experts(topk_ids, token_slot, expert_offsets, row_token, pair_row, row_slot, T,
+                       top_k, num_experts, err_flags=None, stream=None):
+    """Sorts the (token, choice) pairs by expert: offsets, row <-> pair indices
+    and the adapter slot of every sorted row."""
+    op = "lora_group_experts"
+    n = T * top_k
+    (ip, sp, op_, tp, pp, rp, fp), first = _tensors(
+        op, ("topk_ids", topk_ids, "int32", n), ("token_slot", token_slot, "int32", T),
+        ("expert_offsets", expert_offsets, "int32", num_experts + 1),
+        ("row_token", row_token, "int32", n), ("pair_row", pair_row, "int32", n),
+        ("row_slot", row_slot, "int32", n), ("err_flags", err_flags, "int32", 1))
+    fn = (_lib or load()).lora_group_experts
+    _run(op, first, stream,
+         lambda s: fn(ip, sp, op_, tp, pp, rp, T, top_k, num_experts, fp, s))
+
+
+def lora_mx_quantize(x, codes, scales, rows, features, row_index=None, row_count=None,
+                     rows_out=None, activation=LORA_ACT_NONE, x_rows=None, type=None,
+                     err_flags=None, stream=None):
+    """Rows of x (gathered by row_index, or after SwiGLU) as MXFP4 codes and
+    scales.  x_rows: rows of x, by default those of the tensor (with a raw
+    pointer: `rows`)."""
+    op = "lora_mx_quantize"
+    kind = _type_of(op, "x", x, type)
+    pitch = features * (2 if activation == LORA_ACT_SILU_MUL else 1)
+    if x_rows is None:
+        x_rows = rows if x is None or isinstance(x, int) else x.numel() // pitch if pitch > 0 else 0
+    (xp, cp, sp, ip, np_, op_, fp), first = _tensors(
+        op, ("x", x, kind, x_rows * pitch), ("codes", codes, "uint8", rows * features // 2),
+        ("scales", scales, "uint8", rows * features // 32),
+        ("row_index", row_index, "int32", rows), ("row_count", row_count, "int32", 1),
+        ("rows_out", rows_out, kind, rows * features), ("err_flags", err_flags, "int32", 1))
+    fn = (_lib or load()).lora_mx_quantize
+    _run(op, first, stream,
+         lambda s: fn(xp, kind, ip, np_, op_, cp, sp, x_rows, rows, features, activation, fp, s))
+
+
+def lora_mx_dequantize(codes, scales, out, rows, features, type=None, stream=None):
+    """The values that MXFP4 codes and scales stand for."""
+    op = "lora_mx_dequantize"
+    kind = _type_of(op, "out", out, type)
+    (cp, sp, op_), first = _tensors(
+        op, ("codes", codes, "uint8", rows * features // 2),
+        ("scales", scales, "uint8", rows * features // 32), ("out", out, kind, rows * features))
+    fn = (_lib or load()).lora_mx_dequantize
+    _run(op, first, stream, lambda s: fn(cp, sp, op_, kind, rows, features, s))
+
+
+def lora_mx_linear(x_codes, x_scales, w_codes, w_scales, y, rows, in_features, out_features,
+                   type=None, err_flags=None, stream=None):
+    """y = x w^T of MXFP4 operands (a base projection)."""
+    op = "lora_mx_linear"
+    kind = _type_of(op, "y", y, type)
+    (xc, xs, wc, ws, yp, fp), first = _tensors(
+        op, ("x_codes", x_codes, "uint8", rows * in_features // 2),
+        ("x_scales", x_scales, "uint8", rows * in_features // 32),
+        ("w_codes", w_codes, "uint8", out_features * in_features // 2),
+        ("w_scales", w_scales, "uint8", out_features * in_features // 32),
+        ("y", y, kind, rows * out_features), ("err_flags", err_flags, "int32", 1))
+    fn = (_lib or load()).lora_mx_linear
+    _run(op, first, stream,
+         lambda s: fn(xc, xs, wc, ws, yp, kind, rows, in_features, out_features, fp, s))
+
+
+def lora_mx_expert_linear(x_codes, x_scales, w_codes, w_scales, expert_offsets, y, rows_cap,
+                          in_features, out_features, num_experts, type=None, err_flags=None,
+                          stream=None):
+    """The experts' products over rows sorted by expert."""
+    op = "lora_mx_expert_linear"
+    kind = _type_of(op, "y", y, type)
+    n = num_experts * out_features
+    (xc, xs, wc, ws, ep, yp, fp), first = _tensors(
+        op, ("x_codes", x_codes, "uint8", rows_cap * in_features // 2),
+        ("x_scales", x_scales, "uint8", rows_cap * in_features // 32),
+        ("w_codes", w_codes, "uint8", n * in_features // 2),
+        ("w_scales", w_scales, "uint8", n * in_features // 32),
+        ("expert_offsets", expert_offsets, "int32", num_experts + 1),
+        ("y", y, kind, rows_cap * out_features), ("err_flags", err_flags, "int32", 1))
+    fn = (_lib or load()).lora_mx_expert_linear
+    _run(op, first, stream,
+         lambda s: fn(xc, xs, wc, ws, ep, yp, kind, rows_cap, in_features, out_features,
+                      num_experts, fp, s))
+
+
+def lora_combine_experts(y_sorted, pair_row, topk_weights, residual, out, T, top_k, rows_cap,
+                         features, type=None, err_flags=None, stream=None):
+    """Each token's expert rows weighted and added (onto a residual)."""
+    op = "lora_combine_experts"
+    kind = _type_of(op, "out", out, type)
+    (yp, pp, wp, rp, op_, fp), first = _tensors(
+        op, ("y_sorted", y_sorted, kind, rows_cap * features),
+        ("pair_row", pair_row, "int32", T * top_k),
+        ("topk_weights", topk_weights, LORA_TYPE_F32, T * top_k),
+        ("residual", residual, kind, T * features), ("out", out, kind, T * features),
+        ("err_flags", err_flags, "int32", 1))
+    fn = (_lib or load()).lora_combine_experts
+    _run(op, first, stream,
+         lambda s: fn(yp, kind, pp, wp, rp, op_, T, top_k, rows_cap, features, fp, s))
 
 
 def lora_workspace_bytes(op, T, slots, R, num_slices, regime=LORA_REGIME_AUTO):

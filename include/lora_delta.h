@@ -82,6 +82,9 @@ typedef enum {
 #define LORA_FLAG_BAD_PAIR   16u   /* MoE pair_index outside [-1, num_pairs) */
 #define LORA_FLAG_BAD_OFFSETS 32u  /* MoE expert offsets with start < 0, end > rows_cap or end < start */
 #define LORA_FLAG_TIMEOUT    64u   /* a bounded device wait expired; the call's output is incomplete */
+#define LORA_FLAG_BAD_EXPERT 128u  /* grouping: a chosen expert outside [-1, num_experts) */
+#define LORA_FLAG_BAD_ROW    256u  /* a gathered or combined row outside its range */
+#define LORA_FLAG_NONFINITE  512u  /* a NaN or infinity where none has a meaning (routing, quantisation) */
 
 /* Regime hint.  AUTO picks from the scalar shapes only (tokens per slot). */
 #define LORA_REGIME_AUTO 0
@@ -267,6 +270,166 @@ LORA_API lora_status lora_expert_apply(const void* x_sorted, void* y_sorted, con
                               int32_t num_pairs, int32_t R, const int32_t* out_slices,
                               int32_t num_slices, void* workspace, size_t workspace_bytes,
                               uint32_t* err_flags, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The rest of a routed layer: what stands between the router fold
+ * (lora_apply_router, before top-k), the expert fold (lora_expert_apply, on rows
+ * sorted by expert) and the layer's output, and the base products in 4 bits that
+ * the linear and expert folds add to.  In order:
+ *   lora_route_experts    logits -> chosen experts and their weights
+ *   lora_group_experts    (token, choice) pairs sorted by expert
+ *   lora_mx_quantize      rows to 4 bits, copied to their experts' blocks
+ *   lora_mx_expert_linear the experts' product (lora_mx_linear: one weight)
+ *   lora_combine_experts  each token's rows weighted and added
+ * They follow the conventions above, and need no workspace.  `type` is the
+ * element type of the tensors it is said of.
+ * ------------------------------------------------------------------------- */
+#define LORA_TYPE_BF16 0
+#define LORA_TYPE_F16  1
+#define LORA_TYPE_F32  2
+
+#define LORA_SCORE_SOFTMAX 0
+#define LORA_SCORE_SIGMOID 1
+
+#define LORA_GROUP_MAX      0   /* a group's score is its experts' largest key */
+#define LORA_GROUP_TOP_PAIR 1   /* ... the sum of its two largest (of one alone, that one) */
+
+#define LORA_ACT_NONE     0
+#define LORA_ACT_SILU_MUL 1     /* silu(first half of the columns) * second half */
+
+#define LORA_ROUTE_MAX_EXPERTS 1024
+#define LORA_ROUTE_MAX_TOP_K 32
+#define LORA_ROUTE_MAX_GROUPS 32
+
+/*
+ * lora_route_experts -- the selection that the router delta is applied before
+ * (spark_model/lora/expert_apply.rs, module text: "before top-k").
+ *   s[t, e]   = softmax over e, or sigmoid, of logits[t, e]
+ *   key[t, e] = s[t, e] + bias[e]                       (bias NULL: 0)
+ * With num_groups > 1 the experts fall into num_groups equal consecutive groups;
+ * only those of the best top_groups groups (by group_score of their keys) can be
+ * chosen.  topk_ids[t] are the top_k experts of the largest keys, in descending
+ * order; every tie goes to the lowest index.
+ *   topk_weights[t, j] = s[t, id_j] (/ sum over the chosen, if renormalize) * scale
+ * The bias takes part in the choice alone.  The choice is that of exact
+ * arithmetic on the given logits and bias; the weights are computed in fp32.
+ * logits [T, num_experts] of `type`; bias [num_experts] fp32 or NULL; topk_ids
+ * [T, top_k] int32; topk_weights [T, top_k] fp32.
+ * An expert whose logit or bias is -inf is masked: it is never chosen (a masked
+ * logit has score 0).  So is one whose logit or bias is NaN or +inf, which raises
+ * LORA_FLAG_NONFINITE.  A token with fewer than top_k experts to choose from gets
+ * id -1 and weight 0 for the rest.
+ * num_experts <= LORA_ROUTE_MAX_EXPERTS, top_k <= LORA_ROUTE_MAX_TOP_K,
+ * num_groups <= LORA_ROUTE_MAX_GROUPS (LORA_ERR_UNSUPPORTED beyond);
+ * num_groups divides num_experts, 1 <= top_groups <= num_groups and
+ * 1 <= top_k <= num_experts * top_groups / num_groups.
+ */
+LORA_API lora_status lora_route_experts(const void* logits, int32_t type, const float* bias,
+                                        int32_t* topk_ids, float* topk_weights, int32_t T,
+                                        int32_t num_experts, int32_t top_k, int32_t score,
+                                        int32_t num_groups, int32_t top_groups,
+                                        int32_t group_score, int32_t renormalize, float scale,
+                                        uint32_t* err_flags, void* stream);
+
+/*
+ * lora_group_experts -- sorts the T * top_k (token, choice) pairs by expert,
+ * pairs of one expert staying in order: the row order that lora_expert_apply
+ * takes.  With N = expert_offsets[num_experts] rows:
+ *   expert_offsets [num_experts + 1]  rows of expert e: [offsets[e], offsets[e+1])
+ *   row_token [T * top_k]  the token of each of the N sorted rows
+ *   pair_row  [T, top_k]   the row of each pair, -1 where topk_ids is -1
+ *   row_slot  [T * top_k]  token_slot of each sorted row's token (token_slot and
+ *                          row_slot may both be NULL)
+ * all int32.  topk_ids [T, top_k]: -1 takes no row, anything else outside [0,
+ * num_experts) neither, and raises LORA_FLAG_BAD_EXPERT.  row_token and row_slot
+ * beyond the N rows are left as they were.  token_slot [T]: any value, copied.
+ * num_experts <= LORA_ROUTE_MAX_EXPERTS, T * top_k <= 2^30.
+ */
+LORA_API lora_status lora_group_experts(const int32_t* topk_ids, const int32_t* token_slot,
+                                        int32_t* expert_offsets, int32_t* row_token,
+                                        int32_t* pair_row, int32_t* row_slot, int32_t T,
+                                        int32_t top_k, int32_t num_experts,
+                                        uint32_t* err_flags, void* stream);
+
+/*
+ * lora_mx_quantize -- rows to MXFP4 (OCP Microscaling: E2M1 elements, a
+ * power-of-two E8M0 scale for each 32 consecutive ones):
+ *   v     = x[row_index[r]] (row_index NULL: x[r]), or with LORA_ACT_SILU_MUL
+ *           silu(its first `features` columns) * the others, rounded to `type`
+ *   scale = 2^e, e = max(floor(log2(max |v| over the 32)) - 2, -127)
+ *   code  = v / scale rounded to the nearest of 0, .5, 1, 1.5, 2, 3, 4, 6 and
+ *           their negatives (ties to the even code; beyond 6: 6)
+ * exactly.  x [x_rows, features] (SILU_MUL: [x_rows, 2 * features]) of `type`;
+ * codes [rows, features / 2] uint8, element 2i in the low and 2i + 1 in the high
+ * bits of byte i; scales [rows, features / 32] uint8, e + 127; rows_out (or NULL)
+ * [rows, features] of `type`: v itself, such as the expert fold reads.
+ * row_count (device int32, or NULL): only the first *row_count rows are done
+ * (those past it are left as they were), e.g. &expert_offsets[num_experts].
+ * A row_index outside [0, x_rows) skips the row (LORA_FLAG_BAD_ROW).  32 values
+ * with a NaN or an infinity among them become scale byte 255 (NaN) and codes 0
+ * (LORA_FLAG_NONFINITE).  features % 32 == 0.  rows_out must not overlap x.
+ */
+LORA_API lora_status lora_mx_quantize(const void* x, int32_t type, const int32_t* row_index,
+                                      const int32_t* row_count, void* rows_out, uint8_t* codes,
+                                      uint8_t* scales, int32_t x_rows, int32_t rows,
+                                      int32_t features, int32_t activation,
+                                      uint32_t* err_flags, void* stream);
+
+/*
+ * lora_mx_dequantize -- out[r, i] = element i of row r times its scale, rounded
+ * to `type` (bf16 and fp32 hold every one that lora_mx_quantize writes exactly).
+ * Scale byte 255 gives NaN.  Arguments as above; out [rows, features].
+ */
+LORA_API lora_status lora_mx_dequantize(const uint8_t* codes, const uint8_t* scales, void* out,
+                                        int32_t type, int32_t rows, int32_t features,
+                                        void* stream);
+
+/*
+ * lora_mx_linear -- the base product of MXFP4 rows with an MXFP4 weight:
+ *   y[r, n] = sum_k x[r, k] * w[n, k]
+ * x_codes [rows, in_features / 2], x_scales [rows, in_features / 32]; w_codes
+ * [out_features, in_features / 2], w_scales [out_features, in_features / 32], as
+ * lora_mx_quantize writes them (a scale byte above 252 may overflow); y [rows,
+ * out_features] of `type`, written, one rounding of the tensor cores' fp32 sum.
+ * in_features % 32 == 0, out_features % 8 == 0.  The linear delta goes on top:
+ * lora_apply_linear(x, y, ...).
+ */
+LORA_API lora_status lora_mx_linear(const uint8_t* x_codes, const uint8_t* x_scales,
+                                    const uint8_t* w_codes, const uint8_t* w_scales, void* y,
+                                    int32_t type, int32_t rows, int32_t in_features,
+                                    int32_t out_features, uint32_t* err_flags, void* stream);
+
+/*
+ * lora_mx_expert_linear -- the same over rows sorted by expert: row r of
+ * [expert_offsets[e], expert_offsets[e + 1]) with weight e of w_codes
+ * [num_experts, out_features, in_features / 2] and w_scales alike.  x and y have
+ * rows_cap rows; rows of no expert are left as they were.  Offsets as for
+ * lora_expert_apply, which folds the adapters onto y afterwards: an expert with
+ * start < 0, end > rows_cap or end < start is skipped (LORA_FLAG_BAD_OFFSETS).
+ * num_experts <= LORA_ROUTE_MAX_EXPERTS.
+ */
+LORA_API lora_status lora_mx_expert_linear(const uint8_t* x_codes, const uint8_t* x_scales,
+                                           const uint8_t* w_codes, const uint8_t* w_scales,
+                                           const int32_t* expert_offsets, void* y, int32_t type,
+                                           int32_t rows_cap, int32_t in_features,
+                                           int32_t out_features, int32_t num_experts,
+                                           uint32_t* err_flags, void* stream);
+
+/*
+ * lora_combine_experts -- the weighted un-permute that follows the down fold
+ * (spark_model/lora/expert_apply.rs, module text: moe_unpermute_reduce_indexed):
+ *   out[t] = residual[t] + sum_j topk_weights[t, j] * y_sorted[pair_row[t, j]]
+ * in fp32, in order of j, rounded once.  y_sorted [rows_cap, features], residual
+ * [T, features] (or NULL: 0; it may be out itself) and out [T, features] of
+ * `type`; pair_row [T, top_k] as lora_group_experts writes it: -1 adds nothing,
+ * anything else outside [0, rows_cap) neither (LORA_FLAG_BAD_ROW).
+ * features % 8 == 0.
+ */
+LORA_API lora_status lora_combine_experts(const void* y_sorted, int32_t type,
+                                          const int32_t* pair_row, const float* topk_weights,
+                                          const void* residual, void* out, int32_t T,
+                                          int32_t top_k, int32_t rows_cap, int32_t features,
+                                          uint32_t* err_flags, void* stream);
 
 /*
  * lora_apply_linear_noalloc -- lora_apply_linear for callers that cannot give

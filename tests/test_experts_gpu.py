@@ -1,0 +1,493 @@
+"""GPU tests of the routed layer's operators (routing, grouping, MXFP4
+quantisation and product, combine) against the fp64 oracle.
+
+Tolerances.  u = 2^-24 (fp32), h = half a step of the output type.
+  whole numbers, codes, scales and dequantised values: equal.
+  routing weights: an expf (2 u) of a difference of two numbers up to `range`
+    (range * u), a sum of at most E terms in fp32, each within the former
+    ((E / 32 + 5) u for the adding order), a division and a product: relative
+    error at most (2 range + E / 32 + 16) u.
+  product: the tensor cores add in fp32, 64 products a step: K / 64 steps, each
+    dropping at most 2 ulps (2^-22) of the sum of the products' magnitudes so
+    far, then one rounding: (K / 64 + 4) 2^-22 * sum |x w| + h |y|.
+  combine: top_k + 1 fused steps: (top_k + 2) u * sum |w y| + h |out|.
+"""
+import numpy as np
+import pytest
+
+from adapter_lora_serving_b200 import lora as L
+from oracle import experts_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+TYPES = ["bf16", "f16", "f32"]
+
+
+def _torch():
+    import torch
+    return torch
+
+
+def _dtype(name):
+    t = _torch()
+    return {"bf16": t.bfloat16, "f16": t.float16, "f32": t.float32}[name]
+
+
+def _half(name):
+    return _torch().finfo(_dtype(name)).eps / 2
+
+
+def _dev(a, dtype):
+    t = _torch()
+    return t.from_numpy(np.ascontiguousarray(a)).cuda().to(dtype)
+
+
+def _i32(a):
+    t = _torch()
+    return t.from_numpy(np.ascontiguousarray(a, dtype=np.int32)).cuda()
+
+
+def _host(x):
+    return x.double().cpu().numpy()
+
+
+def _rounded(x, name):
+    """fp64 values rounded once to the type (torch goes through fp32)."""
+    eps, tiny = _torch().finfo(_dtype(name)).eps, _torch().finfo(_dtype(name)).smallest_normal
+    step = 2.0 ** np.floor(np.log2(np.maximum(np.abs(x), tiny))) * eps
+    return _host(_torch().from_numpy(np.round(x / step) * step).to(_dtype(name)))
+
+
+def _flags():
+    t = _torch()
+    return t.zeros(1, dtype=t.int32, device="cuda")
+
+
+def _close(got, ref, tol, what):
+    off = np.abs(got - ref) > tol
+    assert not off.any(), (f"{what}: {off.sum()} of {off.size} out of tolerance, first at "
+                           f"{np.argwhere(off)[0]}: {got[off][0]!r} for {ref[off][0]!r}")
+
+
+# ---------------------------------------------------------------------------
+# quantisation
+# ---------------------------------------------------------------------------
+
+def _quantize(x, name, rows, F, index=None, count=None, act=L.LORA_ACT_NONE, keep=False, fill=0x5a):
+    t = _torch()
+    codes = t.full((rows, F // 2), fill, dtype=t.uint8, device="cuda")
+    scales = t.full((rows, F // 32), fill, dtype=t.uint8, device="cuda")
+    out = t.full((rows, F), 3.0, dtype=_dtype(name), device="cuda") if keep else None
+    flags = _flags()
+    L.lora_mx_quantize(x, codes, scales, rows, F, row_index=index, row_count=count, rows_out=out,
+                       activation=act, err_flags=flags)
+    return codes, scales, out, int(flags.item())
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("rows,F", [(1, 32), (3, 64), (37, 2048), (129, 96), (1, 14336)])
+def test_quantize(name, rows, F):
+    rng = np.random.default_rng(rows + F)
+    x = _dev(rng.standard_normal((rows, F)) * np.exp(rng.uniform(-6, 6, (rows, 1))), _dtype(name))
+    codes, scales, _, flags = _quantize(x, name, rows, F)
+    c, s = O.mx_quantize(_host(x))
+    assert (O.unpack(codes.cpu().numpy()) == c).all() and (scales.cpu().numpy() == s).all()
+    assert flags == 0
+
+
+def test_quantize_every_code_border():
+    """Values next to and on every border, signs, zeros, subnormals, the largest
+    finite ones, in fp32."""
+    mids = (O.E2M1[1:] + O.E2M1[:-1]) / 2
+    near = np.concatenate([O.E2M1, mids, np.nextafter(mids.astype(np.float32), 9).astype(np.float64),
+                           np.nextafter(mids.astype(np.float32), 0).astype(np.float64), [7.0, 7.99]])
+    rows = []
+    for e in (0, 5, -30, 120, -120, -126, -128, -140):
+        block = np.zeros(32)
+        block[0] = 4.0                       # holds the scale
+        block[1:31] = np.where(np.arange(30) % 2, 1, -1) * np.resize(near, 30)
+        rows.append(np.concatenate([block, np.resize(near[::-1], 32) * -1]) * 2.0 ** e)
+    rows.append(np.zeros(64))
+    rows.append(np.full(64, -0.0))
+    rows.append(np.full(64, float(np.finfo(np.float32).max)))
+    rows.append(np.full(64, 1.4e-45))
+    x = np.array(rows).astype(np.float32)
+    codes, scales, _, flags = _quantize(_dev(x, _dtype("f32")), "f32", len(x), 64)
+    c, s = O.mx_quantize(x.astype(np.float64))
+    assert (scales.cpu().numpy() == s).all()
+    assert (O.unpack(codes.cpu().numpy()) == c).all() and flags == 0
+
+
+def test_quantize_nonfinite_blocks():
+    x = np.ones((2, 96), dtype=np.float32)
+    x[0, 40] = np.nan
+    x[1, 5] = -np.inf
+    codes, scales, _, flags = _quantize(_dev(x, _dtype("f32")), "f32", 2, 96)
+    c, s = O.mx_quantize(x.astype(np.float64))
+    assert (scales.cpu().numpy() == s).all() and s[0].tolist() == [125, 255, 125]
+    assert (O.unpack(codes.cpu().numpy()) == c).all() and flags == L.LORA_FLAG_NONFINITE
+
+
+@pytest.mark.parametrize("name", TYPES)
+def test_quantize_gather_and_count(name):
+    """Rows taken by index (repeated ones too), a device row count, an index out
+    of range: rows past the count and bad rows stay as they were."""
+    rng = np.random.default_rng(5)
+    x = _dev(rng.standard_normal((9, 160)), _dtype(name))
+    index = rng.integers(0, 9, 50)
+    index[7], index[11] = 9, -1
+    codes, scales, out, flags = _quantize(x, name, 50, 160, _i32(index), _i32([41])[0:], keep=True)
+    rows = np.arange(50)
+    live = (rows < 41) & (index >= 0) & (index < 9)
+    v = _host(x)[np.where(live, index, 0)]
+    c, s = O.mx_quantize(v)
+    got = O.unpack(codes.cpu().numpy())
+    assert (got[live] == c[live]).all() and (scales.cpu().numpy()[live] == s[live]).all()
+    assert (_host(out)[live] == v[live]).all()
+    assert (codes.cpu().numpy()[~live] == 0x5a).all() and (scales.cpu().numpy()[~live] == 0x5a).all()
+    assert (_host(out)[~live] == 3.0).all() and flags == L.LORA_FLAG_BAD_ROW
+
+
+@pytest.mark.parametrize("name", TYPES)
+def test_quantize_silu_mul(name):
+    """SwiGLU rounded once to the type (equal to the fp64 value rounded), then
+    quantised; gate values far out, where the exponential over- or underflows."""
+    rng = np.random.default_rng(6)
+    x = rng.standard_normal((257, 2 * 192)) * 3
+    x[0, :24] = np.linspace(-120, 120, 24)
+    x[1, :8] = [-87, -88.5, -90, -100, 60000, 88.8, 0.0, -0.0]
+    x = _dev(x, _dtype(name))
+    codes, scales, out, flags = _quantize(x, name, 257, 192, act=L.LORA_ACT_SILU_MUL, keep=True)
+    ref = _rounded(O.silu_mul(_host(x)), name)
+    if name == "f32":   # two fp64 formulas, each rounded to fp32
+        _close(_host(out), ref, 2 * U * np.abs(ref), "silu_mul")
+    else:
+        assert (_host(out) == ref).all()
+    c, s = O.mx_quantize(_host(out))
+    assert (O.unpack(codes.cpu().numpy()) == c).all() and (scales.cpu().numpy() == s).all()
+    assert flags == 0
+
+
+@pytest.mark.parametrize("name", TYPES)
+def test_dequantize_every_code_and_scale(name):
+    t = _torch()
+    codes = np.tile(np.arange(32) % 16, (256, 1))
+    scales = np.arange(256)[:, None]
+    out = t.empty(256, 32, dtype=_dtype(name), device="cuda")
+    L.lora_mx_dequantize(_dev(O.pack(codes), t.uint8), _dev(scales, t.uint8), out, 256, 32)
+    with np.errstate(over="ignore"):
+        ref = _host(t.from_numpy(O.mx_values(codes, scales)).float().to(_dtype(name)))
+    assert np.array_equal(_host(out), ref, equal_nan=True)
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+
+def _route(x, bias, k, score="softmax", G=1, g=1, pair=False, renorm=True, scale=1.0):
+    t = _torch()
+    T, E = x.shape
+    ids = t.full((T, k), 77, dtype=t.int32, device="cuda")
+    w = t.full((T, k), -5.0, device="cuda")
+    flags = _flags()
+    L.lora_route_experts(x, bias, ids, w, T, E, k, score=L.LORA_SCORE_SIGMOID if score == "sigmoid"
+                         else L.LORA_SCORE_SOFTMAX, num_groups=G, top_groups=g,
+                         group_score=L.LORA_GROUP_TOP_PAIR if pair else L.LORA_GROUP_MAX,
+                         renormalize=renorm, scale=scale, err_flags=flags)
+    return ids, w, int(flags.item())
+
+
+def _check_route(x, bias, k, **kw):
+    ids, w, flags = _route(x, bias, k, **kw)
+    xh = _host(x)
+    ref_ids, ref_w, ref_flags = O.route(
+        xh, None if bias is None else _host(bias), k, kw.get("score", "softmax"), kw.get("G", 1),
+        kw.get("g", 1), kw.get("pair", False), kw.get("renorm", True), kw.get("scale", 1.0))
+    assert (ids.cpu().numpy() == ref_ids).all(), np.argwhere(ids.cpu().numpy() != ref_ids)[:4]
+    fin = np.where(np.isfinite(xh), np.abs(xh), 0)
+    tol = (4 * fin.max() + x.shape[1] / 32 + 16) * U * np.abs(ref_w) + 2.0 ** -126
+    _close(_host(w), ref_w, tol, "weights")
+    assert flags == ref_flags
+
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(1, 8, 1), (3, 60, 4), (33, 64, 8), (17, 128, 8), (9, 256, 8),
+                                   (5, 160, 6), (4, 512, 10), (3, 1000, 32), (2, 33, 32), (2, 5, 5)])
+def test_route(name, score, T, E, k):
+    rng = np.random.default_rng(E + k)
+    x = _dev(rng.standard_normal((T, E)) * 2, _dtype(name))
+    bias = _dev(rng.standard_normal(E) * 0.1, _dtype("f32"))
+    for renorm, scale in ((True, 1.0), (False, 2.5)):
+        _check_route(x, None, k, score=score, renorm=renorm, scale=scale)
+        _check_route(x, bias, k, score=score, renorm=renorm, scale=scale)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("E,G,g,k", [(256, 8, 4, 8), (64, 8, 3, 6), (60, 4, 2, 5), (96, 3, 1, 4),
+                                     (32, 32, 5, 5), (160, 8, 3, 6), (16, 2, 2, 4), (512, 32, 7, 8)])
+def test_route_groups(score, pair, E, G, g, k):
+    rng = np.random.default_rng(E * G + k)
+    x = _dev(rng.standard_normal((21, E)) * 2, _dtype("bf16"))
+    bias = _dev(rng.standard_normal(E) * 0.2, _dtype("f32"))
+    _check_route(x, None, k, score=score, G=G, g=g, pair=pair)
+    _check_route(x, bias, k, score=score, G=G, g=g, pair=pair, renorm=False)
+
+
+def test_route_ties_go_to_the_lowest_index():
+    t = _torch()
+    for bias in (None, t.zeros(64, device="cuda")):
+        for G, g in ((1, 1), (8, 3)):
+            for pair in (False, True):
+                _check_route(t.zeros(3, 64, device="cuda"), bias, 6, G=G, g=g, pair=pair)
+                x = t.tensor([1.0, 2.0, 1.0, 2.0] * 16, device="cuda").repeat(2, 1).bfloat16()
+                _check_route(x, bias, 6, score="sigmoid", G=G, g=g, pair=pair)
+    x = t.tensor([[0.0, -0.0, 0.0, -0.0]], device="cuda")
+    _check_route(x, None, 3)
+
+
+def test_route_close_scores_as_in_64_bits():
+    """Scores whose fp32 values are equal or swapped: logits one step apart where
+    the sigmoid is flat, biases that undo the difference to a few 2^-40."""
+    t = _torch()
+    x = 15.0 + np.arange(64) * 2.0 ** -20          # 1 - sigmoid ~ 3e-7
+    x = np.stack([x, x[::-1], np.roll(x, 5)])
+    zero = np.zeros(64)
+    _check_route(_dev(x, t.float32), _dev(zero, t.float32), 8, score="sigmoid")
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((200, 64)).astype(np.float32).astype(np.float64)
+    s = np.exp(x - x.max(1, keepdims=True))
+    s /= s.sum(1, keepdims=True)
+    for r in range(0, 200, 40):
+        bias = (0.5 - s[r]).astype(np.float32)     # row r: all keys within 2^-25 of .5
+        _check_route(_dev(x, t.float32), _dev(bias, t.float32), 8)
+        _check_route(_dev(x, t.float32), _dev(bias, t.float32), 4, G=8, g=2, pair=True)
+
+
+def test_route_masked_and_nonfinite():
+    t = _torch()
+    inf, nan = np.inf, np.nan
+    x = np.array([[-inf] * 8, [1, -inf, -inf, 2, -inf, -inf, -inf, -inf],
+                  [1, nan, 3, inf, 0, -1, -inf, 2], [5, 5, 5, 5, 5, 5, 5, 5.0]])
+    for name in ("bf16", "f32"):
+        for kw in (dict(), dict(renorm=False), dict(score="sigmoid"),
+                   dict(score="sigmoid", renorm=False), dict(G=4, g=2), dict(G=4, g=2, pair=True)):
+            for rows in (x[:2], x):
+                _check_route(_dev(rows, _dtype(name)), None, 4, **kw)
+                b = np.array([0, 0, -inf, 0.25, 0, 0, 0, 0])
+                _check_route(_dev(rows, _dtype(name)), _dev(b, t.float32), 4, **kw)
+    b = np.array([0, nan, 0, inf, 0, 0, 0, 0])
+    _check_route(_dev(x[3:], t.float32), _dev(b, t.float32), 8)
+
+
+def test_route_far_logits():
+    """Scores that underflow (softmax) or saturate (sigmoid) in fp32."""
+    t = _torch()
+    x = np.array([[-200.0, -150, -300, -180] * 4, [300.0, 0, -80, -90] * 4,
+                  [90.0, 95, 100, 120] * 4])
+    x = x + np.arange(16) / 8
+    for score in ("softmax", "sigmoid"):
+        _check_route(_dev(x, t.float32), None, 5, score=score)
+    # without renormalisation a score below the smallest fp32 number is 0
+    _check_route(_dev(x, t.float32), None, 5, renorm=False)
+
+
+# ---------------------------------------------------------------------------
+# grouping
+# ---------------------------------------------------------------------------
+
+def _group(ids, slot, E):
+    t = _torch()
+    T, k = ids.shape
+    n = T * k
+    off = t.full((E + 1,), -9, dtype=t.int32, device="cuda")
+    tok, pair, rslot = (t.full((n,), -9, dtype=t.int32, device="cuda") for _ in range(3))
+    flags = _flags()
+    L.lora_group_experts(_i32(ids), None if slot is None else _i32(slot), off, tok, pair,
+                         None if slot is None else rslot, T, k, E, err_flags=flags)
+    return (off.cpu().numpy(), tok.cpu().numpy(), pair.cpu().numpy().reshape(T, k),
+            rslot.cpu().numpy(), int(flags.item()))
+
+
+@pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 128), (37, 8, 128), (700, 3, 60), (2048, 8, 64),
+                                   (513, 8, 1024), (5000, 2, 8), (9000, 4, 256)])
+def test_group(T, k, E):
+    rng = np.random.default_rng(T + k + E)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)])
+    if T > 30:
+        ids[T - T // 10:] = -1                       # a padded batch
+        ids[3, 0], ids[5, k - 1] = E, -2             # out of range
+    slot = rng.integers(-1, 9, T)
+    off, tok, pair, rslot, flags = _group(ids, slot, E)
+    r_off, r_tok, r_pair, r_slot, r_flags = _sorted(ids, slot, E)
+    n = r_off[-1]
+    assert (off == r_off).all() and (tok[:n] == r_tok).all() and (pair == r_pair).all()
+    assert (rslot[:n] == r_slot).all() and flags == r_flags
+    assert (tok[n:] == -9).all() and (rslot[n:] == -9).all()
+
+
+def _sorted(ids, slot, E):
+    """The oracle's grouping by numpy's stable sort (the oracle itself for small
+    sizes)."""
+    T, k = ids.shape
+    if T * k * E < 200000:
+        return O.group(ids, slot, E)
+    flat = ids.reshape(-1)
+    ok = (flat >= 0) & (flat < E)
+    order = np.nonzero(ok)[0][np.argsort(flat[ok], kind="stable")]
+    off = np.concatenate([[0], np.cumsum(np.bincount(flat[ok], minlength=E))])
+    pair = np.full(T * k, -1)
+    pair[order] = np.arange(len(order))
+    bad = ((flat < -1) | (flat >= E)).any()
+    return off, order // k, pair.reshape(T, k), slot[order // k], O.FLAG_BAD_EXPERT if bad else 0
+
+
+def test_group_edges():
+    """No token, no live choice, the same expert twice, no slots."""
+    off, _, _, _, flags = _group(np.zeros((0, 4), dtype=int), np.zeros(0), 12)
+    assert (off == 0).all() and flags == 0
+    off, tok, pair, rslot, flags = _group(np.full((40, 2), -1), np.zeros(40), 12)
+    assert (off == 0).all() and (pair == -1).all() and (tok == -9).all() and (rslot == -9).all()
+    off, tok, pair, _, _ = _group(np.array([[3, 3], [3, 0]]), None, 4)
+    assert off.tolist() == [0, 1, 1, 1, 4] and tok.tolist() == [1, 0, 0, 1]
+    assert pair.tolist() == [[1, 2], [3, 0]]
+
+
+# ---------------------------------------------------------------------------
+# combine
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("T,k,F", [(1, 1, 8), (37, 8, 2048), (5, 9, 24), (200, 4, 168), (3, 32, 64)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_combine(name, T, k, F, residual):
+    rng = np.random.default_rng(T + F)
+    cap = T * k + 3
+    y = _dev(rng.standard_normal((cap, F)), _dtype(name))
+    pair = rng.permutation(cap)[:T * k].reshape(T, k)
+    pair[rng.random((T, k)) < 0.2] = -1
+    if T > 2:
+        pair[1] = -1                                   # a token without rows
+        pair[2, 0] = cap
+    w = _dev(rng.standard_normal((T, k)), _dtype("f32"))
+    res = _dev(rng.standard_normal((T, F)), _dtype(name)) if residual else None
+    t = _torch()
+    out = t.empty(T, F, dtype=_dtype(name), device="cuda")
+    flags = _flags()
+    L.lora_combine_experts(y, _i32(pair), w, res, out, T, k, cap, F, err_flags=flags)
+    ref, mag, ref_flags = O.combine(_host(y), pair, _host(w), None if res is None else _host(res))
+    _close(_host(out), ref, (k + 2) * U * mag + _half(name) * np.abs(ref) + 2.0 ** -133, "combine")
+    assert int(flags.item()) == ref_flags
+    if residual:                                       # in place
+        L.lora_combine_experts(y, _i32(pair), w, res, res, T, k, cap, F)
+        assert t.equal(res, out)
+
+
+# ---------------------------------------------------------------------------
+# products
+# ---------------------------------------------------------------------------
+
+def _operand(rng, *shape, spread=2.0):
+    """Random MXFP4 codes (every code) and scales, packed, on the device; and
+    their values."""
+    t = _torch()
+    codes = rng.integers(0, 16, shape)
+    scales = np.round(127 + spread * rng.standard_normal((*shape[:-1], shape[-1] // 32))).astype(int)
+    return (_dev(O.pack(codes), t.uint8), _dev(scales.astype(np.uint8), t.uint8),
+            O.mx_values(codes, scales))
+
+
+def _tol(name, K, mag, ref):
+    return (K / 64 + 4) * 2.0 ** -22 * mag + _half(name) * np.abs(ref)
+
+
+def _check_linear(name, rows, K, N, seed=0, **kw):
+    t = _torch()
+    rng = np.random.default_rng(seed + rows + K + N)
+    xc, xs, x = _operand(rng, rows, K, **kw)
+    wc, ws, w = _operand(rng, N, K, **kw)
+    y = t.full((rows + 1, N), 7.0, dtype=_dtype(name), device="cuda")
+    flags = _flags()
+    L.lora_mx_linear(xc, xs, wc, ws, y, rows, K, N, err_flags=flags)
+    ref, mag = O.mx_linear(x, w)
+    got = _host(y)
+    assert (got[rows:] == 7.0).all()
+    _close(got[:rows], ref, _tol(name, K, mag, ref), f"linear {rows} {K} {N}")
+    assert int(flags.item()) == 0
+
+
+def test_linear_one_tile_unit_scales():
+    _check_linear("f32", 16, 256, 128, spread=0.0)
+
+
+def test_linear_one_tile():
+    _check_linear("f32", 16, 256, 128)
+
+
+@pytest.mark.parametrize("rows", [1, 7, 16, 17, 33, 64, 65, 128, 129, 300])
+@pytest.mark.parametrize("K,N", [(256, 128), (32, 8), (96, 136), (1056, 264), (2048, 512)])
+def test_linear(rows, K, N):
+    _check_linear("bf16", rows, K, N)
+
+
+@pytest.mark.parametrize("name", ["f16", "f32"])
+@pytest.mark.parametrize("rows,K,N", [(1, 4096, 128), (40, 544, 200), (200, 1024, 384)])
+def test_linear_types(name, rows, K, N):
+    _check_linear(name, rows, K, N, spread=0.5)
+
+
+def test_linear_many_tiles():
+    """Every CTA runs several tiles (rings and accumulators go round)."""
+    _check_linear("bf16", 520, 1280, 8192)
+    _check_linear("bf16", 5, 512, 60000)
+
+
+def test_linear_rerun_bit_exact():
+    t = _torch()
+    rng = np.random.default_rng(9)
+    xc, xs, _ = _operand(rng, 70, 2048)
+    wc, ws, _ = _operand(rng, 640, 2048)
+    ys = [t.empty(70, 640, dtype=t.float32, device="cuda") for _ in range(3)]
+    for y in ys:
+        L.lora_mx_linear(xc, xs, wc, ws, y, 70, 2048, 640)
+    assert t.equal(ys[0], ys[1]) and t.equal(ys[0], ys[2])
+
+
+def _check_expert(name, counts, K, N, seed=0, offsets=None, tail=0, start=0):
+    t = _torch()
+    rng = np.random.default_rng(seed + K + N + len(counts))
+    E = len(counts)
+    if offsets is None:
+        offsets = start + np.concatenate([[0], np.cumsum(counts)])
+    rows = start + int(np.sum(counts)) + tail
+    xc, xs, x = _operand(rng, rows, K)
+    wc, ws, w = _operand(rng, E, N, K)
+    y = t.full((rows, N), 7.0, dtype=_dtype(name), device="cuda")
+    flags = _flags()
+    L.lora_mx_expert_linear(xc, xs, wc, ws, _i32(offsets), y, rows, K, N, E, err_flags=flags)
+    ref, mag, touched, ref_flags = O.mx_expert_linear(x, w, offsets)
+    got = _host(y)
+    assert (got[~touched] == 7.0).all()
+    _close(got[touched], ref[touched], _tol(name, K, mag, ref)[touched], f"experts {counts}")
+    assert int(flags.item()) == ref_flags
+
+
+@pytest.mark.parametrize("counts", [[1], [0, 0, 5, 0], [3, 1, 0, 17, 2, 2], [40, 0, 64, 1],
+                                    [130, 257, 0, 12, 128], [1] * 40, [0, 0, 0]])
+@pytest.mark.parametrize("K,N", [(256, 128), (96, 72), (800, 328)])
+def test_expert_linear(counts, K, N):
+    _check_expert("bf16", counts, K, N)
+
+
+def test_expert_linear_padding_and_types():
+    """Rows before the first and behind the last expert's stay as they were."""
+    for name in TYPES:
+        _check_expert(name, [5, 0, 33, 2], 160, 136, tail=9, start=4)
+    _check_expert("bf16", list(range(0, 130)), 64, 64)
+
+
+def test_expert_linear_bad_offsets_skip_the_expert():
+    _check_expert("bf16", [10, 20, 30], 128, 64, offsets=np.array([-3, 10, 30, 70]))
+    _check_expert("bf16", [10, 20, 30], 128, 64, offsets=np.array([0, 30, 10, 60]))
