@@ -238,75 +238,85 @@ def lora_expert_apply(x_sorted, y_sorted, a, b, pair_index, ranks, scalings, row
 # tensor's type, size, contiguity and device are checked (LORA_ERR_INVALID), its
 # element type picks `type`, and the call runs on the tensors' device and that
 # device's current stream.  Raw device pointers (ints) are passed unchecked, on
-# the current device.
+# the current device.  They are short (a call's host time is that of a small
+# batch's kernel), so the checks are plain loops without closures or objects.
 
-_types = None
+_TYPES = (LORA_TYPE_BF16, LORA_TYPE_F16, LORA_TYPE_F32)
+_torch = None      # the torch module and its element types, once a tensor is given
+_dtypes = None
 
 
-def _type_table():
-    global _types
-    if _types is None:
-        import torch
-        _types = {torch.bfloat16: LORA_TYPE_BF16, torch.float16: LORA_TYPE_F16,
-                  torch.float32: LORA_TYPE_F32, torch.int32: "int32", torch.uint8: "uint8"}
-    return _types
+def _import_torch():
+    global _torch, _dtypes
+    import torch
+    _dtypes = {LORA_TYPE_BF16: torch.bfloat16, LORA_TYPE_F16: torch.float16,
+               LORA_TYPE_F32: torch.float32, "int32": torch.int32, "uint8": torch.uint8}
+    _torch = torch
+    return torch
 
 
 def _refuse(op, what):
     raise LoraError("LORA_ERR_INVALID", f"{op}: {what}")
 
 
-def _run(op, device_of, stream, call):
-    """`call(stream)` on the device of `device_of` (a tensor, or anything else for
-    the current device); raises on a non-OK status."""
-    if stream is not None and not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if device_of is None or isinstance(device_of, int):
-        _check(call(_stream(stream)))
-        return
-    import torch
-    device = device_of.device
-    if device.index == torch.cuda.current_device():
-        _check(call(torch.cuda.current_stream().cuda_stream if stream is None else stream))
-        return
-    with torch.cuda.device(device):
-        _check(call(torch.cuda.current_stream().cuda_stream if stream is None else stream))
-
-
-def _tensors(op, *specs):
-    """Pointers of (name, tensor, kind, least number of elements) and the first
-    tensor among them.  kind: "int32", "uint8", an LORA_TYPE_*, or None (any
-    LORA_TYPE_*)."""
-    table = _types or _type_table()
-    ptrs, first = [], None
-    for name, t, kind, least in specs:
-        if t is None or isinstance(t, int):
+def _pointers(op, tensors, kinds, least, names):
+    """Device pointers of the tensors (None and ints as they are) and the index
+    of their device (None: no tensor among them).  kinds: "int32", "uint8" or an
+    LORA_TYPE_*; least: elements a tensor must have."""
+    ptrs, dev = [], None
+    for i, t in enumerate(tensors):
+        if t is None or t.__class__ is int:
             ptrs.append(t)
             continue
-        got = table.get(t.dtype)
-        if got != kind and (kind is not None or not isinstance(got, int)):
-            _refuse(op, f"{name} has element type {t.dtype}")
-        if first is None:
-            first = t
-            if not t.is_cuda:
-                _refuse(op, f"{name} is not on a CUDA device")
-        elif t.device != first.device:
-            _refuse(op, f"{name} is on {t.device}, not on {first.device}")
+        if _torch is None:
+            _import_torch()
+        if t.dtype is not _dtypes.get(kinds[i]):
+            _refuse(op, f"{names[i]} has element type {t.dtype}")
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                _refuse(op, f"{names[i]} is not on a CUDA device")
+            if dev is not None:
+                _refuse(op, f"{names[i]} is on device {d}, not on {dev}")
+            dev = d
         if not t.is_contiguous():
-            _refuse(op, f"{name} is not contiguous")
-        if t.numel() < least:
-            _refuse(op, f"{name} has {t.numel()} elements, fewer than {least}")
+            _refuse(op, f"{names[i]} is not contiguous")
+        if t.numel() < least[i]:
+            _refuse(op, f"{names[i]} has {t.numel()} elements, fewer than {least[i]}")
         ptrs.append(t.data_ptr())
-    return ptrs, first
+    return ptrs, dev
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) on device `dev` (None: the current one) and `stream`
+    (None: that device's current stream); raises on a non-OK status."""
+    if stream is not None and stream.__class__ is not int:
+        stream = stream.cuda_stream
+    if dev is not None and dev != _torch.cuda.current_device():
+        with _torch.cuda.device(dev):
+            _check(fn(*args, _torch.cuda.current_stream().cuda_stream if stream is None
+                      else stream))
+        return
+    status = fn(*args, _stream(None) if stream is None else stream)
+    if status != LORA_OK:
+        _check(status)
 
 
 def _type_of(op, name, t, given):
-    if given is not None:
-        return given
-    kind = (_types or _type_table()).get(getattr(t, "dtype", None))
-    if not isinstance(kind, int):
-        _refuse(op, f"{name} has no element type of LORA_TYPE_*: give `type` with a raw pointer")
-    return kind
+    """The LORA_TYPE_* of a tensor (`given` for raw pointers)."""
+    if given is None:
+        if _torch is None:
+            _import_torch()
+        dtype = getattr(t, "dtype", None)
+        for kind in _TYPES:
+            if dtype is _dtypes[kind]:
+                return kind
+        _refuse(op, f"{name} has no element type of LORA_TYPE_*"
+                    " (a raw pointer needs the `type` argument)")
+    return given
+
+
+_ROUTE = ("logits", "bias", "topk_ids", "topk_weights", "err_flags")
 
 
 def lora_route_experts(logits, bias, topk_ids, topk_weights, T, num_experts, top_k,
@@ -315,33 +325,34 @@ def lora_route_experts(logits, bias, topk_ids, topk_weights, T, num_experts, top
                        err_flags=None, stream=None):
     """Chosen experts and their weights from routing logits (after
     lora_apply_router)."""
-    op = "lora_route_experts"
-    kind = _type_of(op, "logits", logits, type)
-    (lp, bp, ip, wp, fp), first = _tensors(
-        op, ("logits", logits, kind, T * num_experts), ("bias", bias, LORA_TYPE_F32, num_experts),
-        ("topk_ids", topk_ids, "int32", T * top_k),
-        ("topk_weights", topk_weights, LORA_TYPE_F32, T * top_k),
-        ("err_flags", err_flags, "int32", 1))
-    fn = (_lib or load()).lora_route_experts
-    _run(op, first, stream,
-         lambda s: fn(lp, kind, bp, ip, wp, T, num_experts, top_k, score, num_groups, top_groups,
-                      group_score, 1 if renormalize else 0, scale, fp, s))
+    kind = _type_of("lora_route_experts", "logits", logits, type)
+    n = T * top_k
+    (lp, bp, ip, wp, fp), dev = _pointers(
+        "lora_route_experts", (logits, bias, topk_ids, topk_weights, err_flags),
+        (kind, LORA_TYPE_F32, "int32", LORA_TYPE_F32, "int32"),
+        (T * num_experts, num_experts, n, n, 1), _ROUTE)
+    _call((_lib or load()).lora_route_experts, dev, stream, lp, kind, bp, ip, wp, T, num_experts,
+          top_k, score, num_groups, top_groups, group_score, 1 if renormalize else 0, scale, fp)
+
+
+_GROUP = ("topk_ids", "token_slot", "expert_offsets", "row_token", "pair_row", "row_slot",
+          "err_flags")
 
 
 def lora_group_experts(topk_ids, token_slot, expert_offsets, row_token, pair_row, row_slot, T,
                        top_k, num_experts, err_flags=None, stream=None):
     """Sorts the (token, choice) pairs by expert: offsets, row <-> pair indices
     and the adapter slot of every sorted row."""
-    op = "lora_group_experts"
     n = T * top_k
-    (ip, sp, op_, tp, pp, rp, fp), first = _tensors(
-        op, ("topk_ids", topk_ids, "int32", n), ("token_slot", token_slot, "int32", T),
-        ("expert_offsets", expert_offsets, "int32", num_experts + 1),
-        ("row_token", row_token, "int32", n), ("pair_row", pair_row, "int32", n),
-        ("row_slot", row_slot, "int32", n), ("err_flags", err_flags, "int32", 1))
-    fn = (_lib or load()).lora_group_experts
-    _run(op, first, stream,
-         lambda s: fn(ip, sp, op_, tp, pp, rp, T, top_k, num_experts, fp, s))
+    (ip, sp, op, tp, pp, rp, fp), dev = _pointers(
+        "lora_group_experts",
+        (topk_ids, token_slot, expert_offsets, row_token, pair_row, row_slot, err_flags),
+        ("int32",) * 7, (n, T, num_experts + 1, n, n, n, 1), _GROUP)
+    _call((_lib or load()).lora_group_experts, dev, stream, ip, sp, op, tp, pp, rp, T, top_k,
+          num_experts, fp)
+
+
+_QUANTIZE = ("x", "codes", "scales", "row_index", "row_count", "rows_out", "err_flags")
 
 
 def lora_mx_quantize(x, codes, scales, rows, features, row_index=None, row_count=None,
@@ -350,82 +361,80 @@ def lora_mx_quantize(x, codes, scales, rows, features, row_index=None, row_count
     """Rows of x (gathered by row_index, or after SwiGLU) as MXFP4 codes and
     scales.  x_rows: rows of x, by default those of the tensor (with a raw
     pointer: `rows`)."""
-    op = "lora_mx_quantize"
-    kind = _type_of(op, "x", x, type)
-    pitch = features * (2 if activation == LORA_ACT_SILU_MUL else 1)
+    kind = _type_of("lora_mx_quantize", "x", x, type)
+    pitch = features * 2 if activation == LORA_ACT_SILU_MUL else features
     if x_rows is None:
-        x_rows = rows if x is None or isinstance(x, int) else x.numel() // pitch if pitch > 0 else 0
-    (xp, cp, sp, ip, np_, op_, fp), first = _tensors(
-        op, ("x", x, kind, x_rows * pitch), ("codes", codes, "uint8", rows * features // 2),
-        ("scales", scales, "uint8", rows * features // 32),
-        ("row_index", row_index, "int32", rows), ("row_count", row_count, "int32", 1),
-        ("rows_out", rows_out, kind, rows * features), ("err_flags", err_flags, "int32", 1))
-    fn = (_lib or load()).lora_mx_quantize
-    _run(op, first, stream,
-         lambda s: fn(xp, kind, ip, np_, op_, cp, sp, x_rows, rows, features, activation, fp, s))
+        x_rows = rows if x is None or x.__class__ is int or pitch <= 0 else x.numel() // pitch
+    n = rows * features
+    (xp, cp, sp, ip, np, op, fp), dev = _pointers(
+        "lora_mx_quantize", (x, codes, scales, row_index, row_count, rows_out, err_flags),
+        (kind, "uint8", "uint8", "int32", "int32", kind, "int32"),
+        (x_rows * pitch, n // 2, n // 32, rows, 1, n, 1), _QUANTIZE)
+    _call((_lib or load()).lora_mx_quantize, dev, stream, xp, kind, ip, np, op, cp, sp, x_rows,
+          rows, features, activation, fp)
+
+
+_DEQUANTIZE = ("codes", "scales", "out")
 
 
 def lora_mx_dequantize(codes, scales, out, rows, features, type=None, stream=None):
     """The values that MXFP4 codes and scales stand for."""
-    op = "lora_mx_dequantize"
-    kind = _type_of(op, "out", out, type)
-    (cp, sp, op_), first = _tensors(
-        op, ("codes", codes, "uint8", rows * features // 2),
-        ("scales", scales, "uint8", rows * features // 32), ("out", out, kind, rows * features))
-    fn = (_lib or load()).lora_mx_dequantize
-    _run(op, first, stream, lambda s: fn(cp, sp, op_, kind, rows, features, s))
+    kind = _type_of("lora_mx_dequantize", "out", out, type)
+    n = rows * features
+    (cp, sp, op), dev = _pointers("lora_mx_dequantize", (codes, scales, out),
+                                  ("uint8", "uint8", kind), (n // 2, n // 32, n), _DEQUANTIZE)
+    _call((_lib or load()).lora_mx_dequantize, dev, stream, cp, sp, op, kind, rows, features)
+
+
+_LINEAR = ("x_codes", "x_scales", "w_codes", "w_scales", "y", "err_flags")
 
 
 def lora_mx_linear(x_codes, x_scales, w_codes, w_scales, y, rows, in_features, out_features,
                    type=None, err_flags=None, stream=None):
     """y = x w^T of MXFP4 operands (a base projection)."""
-    op = "lora_mx_linear"
-    kind = _type_of(op, "y", y, type)
-    (xc, xs, wc, ws, yp, fp), first = _tensors(
-        op, ("x_codes", x_codes, "uint8", rows * in_features // 2),
-        ("x_scales", x_scales, "uint8", rows * in_features // 32),
-        ("w_codes", w_codes, "uint8", out_features * in_features // 2),
-        ("w_scales", w_scales, "uint8", out_features * in_features // 32),
-        ("y", y, kind, rows * out_features), ("err_flags", err_flags, "int32", 1))
-    fn = (_lib or load()).lora_mx_linear
-    _run(op, first, stream,
-         lambda s: fn(xc, xs, wc, ws, yp, kind, rows, in_features, out_features, fp, s))
+    kind = _type_of("lora_mx_linear", "y", y, type)
+    n, m = rows * in_features, out_features * in_features
+    (xc, xs, wc, ws, yp, fp), dev = _pointers(
+        "lora_mx_linear", (x_codes, x_scales, w_codes, w_scales, y, err_flags),
+        ("uint8", "uint8", "uint8", "uint8", kind, "int32"),
+        (n // 2, n // 32, m // 2, m // 32, rows * out_features, 1), _LINEAR)
+    _call((_lib or load()).lora_mx_linear, dev, stream, xc, xs, wc, ws, yp, kind, rows,
+          in_features, out_features, fp)
+
+
+_EXPERT_LINEAR = ("x_codes", "x_scales", "w_codes", "w_scales", "expert_offsets", "y", "err_flags")
 
 
 def lora_mx_expert_linear(x_codes, x_scales, w_codes, w_scales, expert_offsets, y, rows_cap,
                           in_features, out_features, num_experts, type=None, err_flags=None,
                           stream=None):
     """The experts' products over rows sorted by expert."""
-    op = "lora_mx_expert_linear"
-    kind = _type_of(op, "y", y, type)
-    n = num_experts * out_features
-    (xc, xs, wc, ws, ep, yp, fp), first = _tensors(
-        op, ("x_codes", x_codes, "uint8", rows_cap * in_features // 2),
-        ("x_scales", x_scales, "uint8", rows_cap * in_features // 32),
-        ("w_codes", w_codes, "uint8", n * in_features // 2),
-        ("w_scales", w_scales, "uint8", n * in_features // 32),
-        ("expert_offsets", expert_offsets, "int32", num_experts + 1),
-        ("y", y, kind, rows_cap * out_features), ("err_flags", err_flags, "int32", 1))
-    fn = (_lib or load()).lora_mx_expert_linear
-    _run(op, first, stream,
-         lambda s: fn(xc, xs, wc, ws, ep, yp, kind, rows_cap, in_features, out_features,
-                      num_experts, fp, s))
+    kind = _type_of("lora_mx_expert_linear", "y", y, type)
+    n, m = rows_cap * in_features, num_experts * out_features * in_features
+    (xc, xs, wc, ws, ep, yp, fp), dev = _pointers(
+        "lora_mx_expert_linear",
+        (x_codes, x_scales, w_codes, w_scales, expert_offsets, y, err_flags),
+        ("uint8", "uint8", "uint8", "uint8", "int32", kind, "int32"),
+        (n // 2, n // 32, m // 2, m // 32, num_experts + 1, rows_cap * out_features, 1),
+        _EXPERT_LINEAR)
+    _call((_lib or load()).lora_mx_expert_linear, dev, stream, xc, xs, wc, ws, ep, yp, kind,
+          rows_cap, in_features, out_features, num_experts, fp)
+
+
+_COMBINE = ("y_sorted", "pair_row", "topk_weights", "residual", "out", "err_flags")
 
 
 def lora_combine_experts(y_sorted, pair_row, topk_weights, residual, out, T, top_k, rows_cap,
                          features, type=None, err_flags=None, stream=None):
     """Each token's expert rows weighted and added (onto a residual)."""
-    op = "lora_combine_experts"
-    kind = _type_of(op, "out", out, type)
-    (yp, pp, wp, rp, op_, fp), first = _tensors(
-        op, ("y_sorted", y_sorted, kind, rows_cap * features),
-        ("pair_row", pair_row, "int32", T * top_k),
-        ("topk_weights", topk_weights, LORA_TYPE_F32, T * top_k),
-        ("residual", residual, kind, T * features), ("out", out, kind, T * features),
-        ("err_flags", err_flags, "int32", 1))
-    fn = (_lib or load()).lora_combine_experts
-    _run(op, first, stream,
-         lambda s: fn(yp, kind, pp, wp, rp, op_, T, top_k, rows_cap, features, fp, s))
+    kind = _type_of("lora_combine_experts", "out", out, type)
+    n, m = T * top_k, T * features
+    (yp, pp, wp, rp, op, fp), dev = _pointers(
+        "lora_combine_experts", (y_sorted, pair_row, topk_weights, residual, out, err_flags),
+        (kind, "int32", LORA_TYPE_F32, kind, kind, "int32"),
+        (rows_cap * features, n, n, m, m, 1), _COMBINE)
+    _call((_lib or load()).lora_combine_experts, dev, stream, yp, kind, pp, wp, rp, op, T, top_k,
+          rows_cap, features, fp)
 
 
 def lora_workspace_bytes(op, T, slots, R, num_slices, regime=LORA_REGIME_AUTO):

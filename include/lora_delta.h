@@ -405,7 +405,8 @@ LORA_API lora_status lora_mx_linear(const uint8_t* x_codes, const uint8_t* x_sca
  * [num_experts, out_features, in_features / 2] and w_scales alike.  x and y have
  * rows_cap rows; rows of no expert are left as they were.  Offsets as for
  * lora_expert_apply, which folds the adapters onto y afterwards: an expert with
- * start < 0, end > rows_cap or end < start is skipped (LORA_FLAG_BAD_OFFSETS).
+ * start < 0, end > rows_cap or end < start is skipped (LORA_FLAG_BAD_OFFSETS);
+ * blocks that overlap give an unspecified result for the shared rows.
  * num_experts <= LORA_ROUTE_MAX_EXPERTS.
  */
 LORA_API lora_status lora_mx_expert_linear(const uint8_t* x_codes, const uint8_t* x_scales,
