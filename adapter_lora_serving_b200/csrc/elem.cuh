@@ -31,6 +31,11 @@ LORA_DEV float2 unpack2(__half, uint32_t v) {
   return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
+// pack2 where a template also names it for fp32 (and never calls it there).
+template <typename T>
+LORA_DEV uint32_t pack2_any(T t, float lo, float hi) { return pack2(t, lo, hi); }
+LORA_DEV uint32_t pack2_any(float, float lo, float) { return __float_as_uint(lo); }
+
 // Eight consecutive elements as raw words (16-byte accesses; two for fp32).
 template <typename T>
 struct Raw8 {

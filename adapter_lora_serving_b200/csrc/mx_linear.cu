@@ -38,83 +38,122 @@ namespace lora {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kM = 128;               // features per tile
-constexpr int kK = 256;               // elements of k per stage
+constexpr int kK = 256;               // elements of k per stage of element tiles
 constexpr int kATile = kM * kK / 2;   // 16 KB
+constexpr int kBlockK = 512;          // elements of k per block of scales (16 bytes a row)
 constexpr int kSfAtom = 512;          // scales of 128 rows x 128 elements
-constexpr int kAhead = 4;             // stages of scales fetched ahead
+constexpr int kSfSlots = 3;           // blocks of scales in flight
 constexpr int kHeader = 6144;         // barriers, scan scratch and the experts' tile prefix (1025 ints)
 
 template <int BN>
 struct Cfg {
   static constexpr int kBTile = BN * kK / 2;
-  static constexpr int kSfBytes = 4 * kSfAtom;   // two atoms of each operand
-  static constexpr int kStage = kATile + kBTile + kSfBytes;
-  static constexpr int kStages = BN >= 128 ? 6 : BN >= 64 ? 8 : 9;
-  static constexpr int kSmem = 1024 + kHeader + kStages * kStage;   // 1024: alignment slack
-  // two accumulators, then two sets of scales (8 columns each of W and of X)
-  static constexpr int kCols = 2 * BN + 32 <= 64 ? 64 : 2 * BN + 32 <= 128 ? 128 : 2 * BN + 32 <= 256 ? 256 : 512;
+  static constexpr int kStage = kATile + kBTile;
+  static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : BN >= 64 ? 8 : 9;
+  static constexpr int kAtoms = BN > 128 ? 2 : 1;             // of x, per 128 elements of k
+  static constexpr int kSfX = 4 * kAtoms * kSfAtom;
+  static constexpr int kSfSlot = 4 * kSfAtom + kSfX;
+  static constexpr int kSmem = 1024 + kHeader + kStages * kStage + kSfSlots * kSfSlot;   // 1024: alignment slack
+  static constexpr int kAcc = BN > 128 ? 1 : 2;               // accumulators
+  static constexpr int kSfCols = 16 + 16 * kAtoms;            // tensor memory columns of a block of scales
+  static constexpr int kUsed = kAcc * BN + 2 * kSfCols;
+  static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+  static constexpr int kEpiWarps = BN >= 64 ? 8 : 4;
+  static constexpr int kWarpCols = BN >= 64 ? BN / 2 : 32;    // columns an epilogue warp drains
+  static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
 struct Params {
   MxLinearParams q;
   int ftiles;       // feature tiles of a weight
   int splits;       // CTAs per tile (the cluster size)
-  int kstages;      // stages of the whole k
-  int per_split;    // stages of a CTA's part
+  int blocks;       // 512-element blocks of the whole k
+  int per_split;    // blocks of a CTA's part
+  int tma_scales;   // scales come by tensor TMA (their rows are multiples of 16 bytes)
 };
 
 LORA_DEV uint32_t up1024(uint32_t v) { return (v + 1023u) & ~1023u; }
 
-// Wait that also gives up when another role of the CTA has.
+// Wait that also gives up when another role of the CTA has.  The clock is looked
+// at only now and then.
 LORA_DEV bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, uint32_t* flags) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
     if (*stop) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      *stop = 1;
-      raise_flag(flags, LORA_FLAG_TIMEOUT);
-      return false;
+    if ((i & 255u) == 0u) {
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) {
+        *stop = 1;
+        raise_flag(flags, LORA_FLAG_TIMEOUT);
+        return false;
+      }
     }
   }
   return true;
 }
-LORA_DEV bool warp_wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop,
-                                uint32_t* flags) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = wait_or_stop(bar, parity, stop, flags) ? 1 : 0;
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
+// A ring position and the parity of its current round.
+struct Ring {
+  int s = 0;
+  uint32_t round = 0;
+  template <int N>
+  LORA_DEV void next() {
+    if (++s == N) {
+      s = 0;
+      round ^= 1u;
+    }
+  }
+};
 
 // Instruction descriptor of kind::mxf4: both operands E2M1 (1) and K-major,
 // scales UE8M0, 64 elements of k; `half` picks the lower or upper two bytes of
 // the scale words.
-LORA_DEV uint32_t mxf4_idesc(int N, uint32_t half) {
+constexpr uint32_t mxf4_idesc(int N, uint32_t half) {
   return ((half * 2u) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
          ((uint32_t)(kM >> 7) << 27) | ((half * 2u) << 29);
 }
 
-LORA_DEV void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+// Shared-memory matrix descriptors: the low word holds the address / 16 (and the
+// unused leading offset), the high word is a constant.
+constexpr uint32_t kDescTile = (1024u >> 4) | (1u << 14) | (2u << 29);  // 8 rows of 128 bytes, 128-byte swizzle
+constexpr uint32_t kDescScale = (128u >> 4) | (1u << 14);               // 8 rows of 16 bytes, no swizzle
+LORA_DEV uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
+
+LORA_DEV void mma_mxf4(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t sfa,
                        uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %7};\n\t"
+      "mov.b64 b, {%2, %7};\n\t"
       "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
-      "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      "[%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(kDescTile)
       : "memory");
 }
 
 // 32 rows of 16 bytes from shared memory to four columns of tensor memory, the
 // same in each quarter of the lanes.
-LORA_DEV void copy_scales(uint32_t taddr, uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-  d |= (uint64_t)1u << 16;          // leading byte offset (one 16-byte column: unused)
-  d |= (uint64_t)(128u >> 4) << 32; // eight rows of 16 bytes to the next eight
-  d |= (uint64_t)1u << 46;          // descriptor version; no swizzle
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+LORA_DEV void copy_scales(uint32_t taddr, uint32_t lo) {
+  asm volatile(
+      "{\n\t.reg .b64 d;\n\t"
+      "mov.b64 d, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+      "r"(lo), "r"(kDescScale)
+      : "memory");
+}
+
+// One lane of the (converged) warp.
+LORA_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // A tile: `rows` rows of x from row0 on times the 128 weight rows from wrow on.
@@ -148,63 +187,98 @@ LORA_DEV Tile tile_of(const Params& p, const Plan& plan, int u) {
   return t;
 }
 
-// Eight scale bytes (256 elements of k) of a row as two words, zero past the end.
-LORA_DEV uint2 load_scales(const uint8_t* base, long long row, long long rows, int per_row, int at) {
-  uint2 v = make_uint2(0u, 0u);
-  if (row >= rows || at >= per_row) return v;
-  const uint8_t* s = base + row * per_row + at;
-  if ((per_row & 7) == 0) return __ldg(reinterpret_cast<const uint2*>(s));
-  const int n = min(8, per_row - at);
-  if ((per_row & 3) == 0) {
-    v.x = __ldg(reinterpret_cast<const uint32_t*>(s));
-    if (n > 4) v.y = __ldg(reinterpret_cast<const uint32_t*>(s) + 1);
-    return v;
+// The 16 scale bytes of a row's block from byte `at` on, zero past its end.
+LORA_DEV uint4 load_scales(const uint8_t* base, long long row, long long rows, int per_row, int at) {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  if (row < rows) {
+    const uint8_t* s = base + row * per_row + at;
+    const int n = min(16, per_row - at);
+    if ((per_row & 7) == 0) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(s));
+      w[0] = u.x;
+      w[1] = u.y;
+      if (n > 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(s) + 1);
+        w[2] = v.x;
+        w[3] = v.y;
+      }
+    } else if ((per_row & 3) == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (4 * i < n) w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < n) w[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
+    }
   }
-  for (int i = 0; i < n; ++i) {
-    const uint32_t b = __ldg(s + i);
-    if (i < 4) v.x |= b << (8 * i);
-    else v.y |= b << (8 * (i - 4));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A thread's 32 columns of its feature, tokens [0, rows), to y.  16-bit types:
+// neighbouring lanes trade halves, so that each stores two features at once.
+template <typename OT>
+LORA_DEV void store_columns(OT* y, int N, int f, bool f_ok, int rows, const uint32_t (&v)[16]) {
+  const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1;
+  // N is a multiple of 8, so a feature and its neighbour are valid together
+  OT* o = y + (f - (odd ? 1 : 0)) + (odd ? (size_t)N : (size_t)0);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, v[i], 1);
+    const uint32_t out = odd ? __byte_perm(other, v[i], 0x7632) : __byte_perm(v[i], other, 0x5410);
+    if (f_ok && 2 * i + (odd ? 1 : 0) < rows)
+      *reinterpret_cast<uint32_t*>(o + (size_t)(2 * i) * N) = out;
   }
-  return v;
 }
 
 template <int BN, typename OT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<BN>::kThreads, 1)
 mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                 const Params p) {
+                 const __grid_constant__ CUtensorMap map_ws,
+                 const __grid_constant__ CUtensorMap map_xs, const Params p) {
   typedef Cfg<BN> C;
   constexpr int kS = C::kStages;
   extern __shared__ uint8_t mx_smem[];
   uint8_t* base = mx_smem + (up1024(smem_u32(mx_smem)) - smem_u32(mx_smem));
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
   uint64_t* empty = full + kS;
-  uint64_t* accfull = empty + kS;
+  uint64_t* sf_raw = empty + kS;            // a block of scales has landed (by TMA)
+  uint64_t* sf_full = sf_raw + kSfSlots;    // ... is in order
+  uint64_t* sf_empty = sf_full + kSfSlots;  // ... is in tensor memory
+  uint64_t* accfull = sf_empty + kSfSlots;
   uint64_t* accempty = accfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 512);
   volatile int* stop = reinterpret_cast<volatile int*>(base + 516);
   int* scratch = reinterpret_cast<int*>(base + 576);
   int* prefix = reinterpret_cast<int*>(base + 1024);   // up to 1025 ints
   uint8_t* ring = base + kHeader;
-  auto a_tile = [&](int s) { return ring + s * C::kStage; };
-  auto b_tile = [&](int s) { return ring + s * C::kStage + kATile; };
-  auto sf_tile = [&](int s) { return ring + s * C::kStage + kATile + C::kBTile; };
+  uint8_t* sf_ring = ring + kS * C::kStage;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = p.splits;
   const int part = splits > 1 ? (int)cluster_ctarank() : 0;
   const int first_unit = (int)blockIdx.x / splits;
   const int unit_step = (int)gridDim.x / splits;
-  const int ks0 = part * p.per_split;
-  const int kst = min(p.kstages - ks0, p.per_split);   // >= 1
+  const int block0 = part * p.per_split;
+  const int blocks = min(p.blocks - block0, p.per_split);                  // >= 1
+  const int k0 = block0 * kBlockK;
+  const int kcount = min(p.q.K - k0, blocks * kBlockK);                    // this CTA's part of k
+  const int stages = (kcount + kK - 1) / kK;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kS; ++i) {
-      mbar_init(&full[i], 3);    // the producer and the two scale warps
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kSfSlots; ++i) {
+      mbar_init(&sf_raw[i], 1);
+      mbar_init(&sf_full[i], 2);    // the two scale warps
+      mbar_init(&sf_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&accfull[i], 1);
-      mbar_init(&accempty[i], 4);
+      mbar_init(&accempty[i], C::kEpiWarps);
     }
     *stop = 0;
     fence_mbar_init();
@@ -224,7 +298,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     int carry = 0;
     uint32_t bad = 0;
     if (threadIdx.x == 0) prefix[0] = 0;
-    for (int e0 = 0; e0 < p.q.experts; e0 += kThreads) {
+    for (int e0 = 0; e0 < p.q.experts; e0 += C::kThreads) {
       const int e = e0 + threadIdx.x;
       int cnt = 0;
       if (e < p.q.experts) {
@@ -233,7 +307,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         else cnt = (hi - lo + BN - 1) / BN * p.ftiles;
       }
       int tot;
-      const int inc = block_inclusive_scan<kThreads>(cnt, scratch, &tot);
+      const int inc = block_inclusive_scan<C::kThreads>(cnt, scratch, &tot);
       if (e < p.q.experts) prefix[e + 1] = carry + inc;
       carry += tot;
     }
@@ -245,137 +319,192 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int units = plan.tiles > first_unit ? (plan.tiles - first_unit - 1) / unit_step + 1 : 0;
-  const int total = units * kst;    // stages this CTA runs
 
-  // ---- roles; `g` counts stages over all units, so rings and phases run on ----
   if (warp == 0) {
-    if (lane == 0) {
-      int g = 0;
+    // ---- element tiles and raw scales ----
+    if (elect_one()) {
+      Ring r, b;
       for (int i = 0; i < units && !*stop; ++i) {
         const Tile t = tile_of<BN>(p, plan, first_unit + i * unit_step);
-        for (int k = 0; k < kst; ++k, ++g) {
-          const int s = g % kS;
-          if (g >= kS && !wait_or_stop(&empty[s], (uint32_t)((g / kS - 1) & 1), stop, p.q.flags)) break;
-          mbar_arrive_expect_tx(&full[s], kATile + C::kBTile);
-          tma_load_2d(a_tile(s), &map_w, (ks0 + k) * (kK / 2), t.wrow, &full[s]);
-          tma_load_2d(b_tile(s), &map_x, (ks0 + k) * (kK / 2), t.row0, &full[s]);
+        for (int k = 0; k < stages; ++k) {
+          if ((k & 1) == 0 && p.tma_scales) {
+            if (!wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags)) break;
+            uint8_t* slot = sf_ring + b.s * C::kSfSlot;
+            const int at = (k0 + k * kK) / 32;
+            mbar_arrive_expect_tx(&sf_raw[b.s], (kM + BN) * 16);
+            tma_load_2d(slot, &map_ws, at, t.wrow, &sf_raw[b.s]);
+            tma_load_2d(slot + 4 * kSfAtom, &map_xs, at, t.row0, &sf_raw[b.s]);
+            b.next<kSfSlots>();
+          }
+          if (!wait_or_stop(&empty[r.s], r.round ^ 1u, stop, p.q.flags)) break;
+          uint8_t* slot = ring + r.s * C::kStage;
+          const int at = (k0 + k * kK) / 2;
+          mbar_arrive_expect_tx(&full[r.s], C::kStage);
+          tma_load_2d(slot, &map_w, at, t.wrow, &full[r.s]);
+          tma_load_2d(slot + kATile, &map_x, at, t.row0, &full[r.s]);
+          r.next<kS>();
         }
       }
     }
   } else if (warp == 1) {
-    int g = 0;
-    for (int i = 0; i < units; ++i) {
-      const int acc = i & 1;
-      if (i >= 2 && !warp_wait_or_stop(&accempty[acc], (uint32_t)((i / 2 - 1) & 1), stop, p.q.flags)) break;
-      tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)(acc * BN);
+    // ---- MMAs: one thread ----
+    if (elect_one()) {
+      Ring r, b, acc;
+      const uint32_t ring_lo = desc_lo(smem_u32(ring)), sf_lo = desc_lo(smem_u32(sf_ring));
       bool ok = true;
-      for (int k = 0; k < kst; ++k, ++g) {
-        const int s = g % kS;
-        if (!(ok = warp_wait_or_stop(&full[s], (uint32_t)((g / kS) & 1), stop, p.q.flags))) break;
+      for (int i = 0; i < units && ok; ++i) {
+        if (!(ok = wait_or_stop(&accempty[acc.s], acc.round ^ 1u, stop, p.q.flags))) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t sf = tmem + (uint32_t)(2 * BN + (g & 1) * 16);
-          const uint32_t ssf = smem_u32(sf_tile(s));
-          const int steps = min(4, (p.q.K - (ks0 + k) * kK + 63) / 64);
-          for (int c = 0; c < 2; ++c) {
-            copy_scales(sf + 4 * c, ssf + c * kSfAtom);
-            copy_scales(sf + 8 + 4 * c, ssf + (2 + c) * kSfAtom);
+        const uint32_t d = tmem + (uint32_t)(acc.s * BN);
+        uint32_t sf = 0;
+        for (int k = 0; k < stages; ++k) {
+          if ((k & 1) == 0) {
+            if (!(ok = wait_or_stop(&sf_full[b.s], b.round, stop, p.q.flags))) break;
+            tc_fence_after();
+            // the two blocks of scales in tensor memory take turns with the MMAs
+            // in issue order: copies and MMAs of one thread run in order
+            sf = tmem + (uint32_t)(C::kAcc * BN + (k & 2 ? C::kSfCols : 0));
+            const uint32_t lo = sf_lo + (uint32_t)b.s * (C::kSfSlot >> 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              copy_scales(sf + 4 * c, lo + c * (kSfAtom >> 4));
+#pragma unroll
+              for (int h = 0; h < C::kAtoms; ++h)
+                copy_scales(sf + 16 + 4 * (C::kAtoms * c + h),
+                            lo + (4 + C::kAtoms * c + h) * (kSfAtom >> 4));
+            }
+            mma_commit(&sf_empty[b.s]);
+            b.next<kSfSlots>();
           }
-          const uint32_t sa = smem_u32(a_tile(s)), sb = smem_u32(b_tile(s));
-          for (int j = 0; j < steps; ++j)
-            mma_mxf4(d, smem_desc_kmajor(sa + j * 32, 128), smem_desc_kmajor(sb + j * 32, 128),
-                     mxf4_idesc(BN, (uint32_t)(j & 1)), sf + 4 * (j >> 1), sf + 8 + 4 * (j >> 1),
-                     (k > 0 || j > 0) ? 1u : 0u);
-          mma_commit(&empty[s]);
+          if (!(ok = wait_or_stop(&full[r.s], r.round, stop, p.q.flags))) break;
+          tc_fence_after();
+          const uint32_t a_lo = ring_lo + (uint32_t)r.s * (C::kStage >> 4);
+          const uint32_t b_lo = a_lo + (kATile >> 4);
+          const uint32_t sfk = sf + (k & 1 ? 8u : 0u), sfx = sf + 16u + (k & 1 ? 8u * C::kAtoms : 0u);
+          const int left = kcount - k * kK;   // elements of k from this stage on
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (j == 0 || left > 64 * j)
+              mma_mxf4(d, a_lo + 2 * j, b_lo + 2 * j, mxf4_idesc(BN, j & 1), sfk + 4 * (j >> 1),
+                       sfx + 4 * C::kAtoms * (j >> 1), (k | j) != 0 ? 1u : 0u);
+          mma_commit(&empty[r.s]);
+          r.next<kS>();
         }
-        __syncwarp();
+        if (!ok) break;
+        mma_commit(&accfull[acc.s]);
+        acc.next<C::kAcc>();
       }
-      if (!ok) break;
-      if (lane == 0) mma_commit(&accfull[acc]);
-      __syncwarp();
     }
   } else if (warp < 4) {
-    // scales: warp 2 the weight's 128 rows, warp 3 the BN rows of x.  Lane l has
-    // rows l, l + 32, l + 64, l + 96 of the tile.
+    // ---- scales into the tensor core's order: warp 2 the weight's 128 rows, warp
+    // 3 those of x.  Lane l has rows l, l + 32, l + 64, l + 96 of an atom; a row's
+    // 16 bytes are one word for each of four atoms. ----
     const bool of_w = warp == 2;
-    const uint8_t* src = of_w ? p.q.w_scales : p.q.x_scales;
-    const long long nrows = of_w ? (long long)max(p.q.experts, 1) * p.q.N : p.q.rows;
-    const int per_row = p.q.K / 32;
-    const int nj = of_w ? 4 : (BN + 31) / 32;
-    uint2 buf[kAhead][4];
-    int li = 0, lk = 0;   // next stage to fetch
-    long long row = 0;
-    auto fetch = [&](uint2 (&v)[4]) {
-      if (li < units) {
-        if (lk == 0) {
-          const Tile t = tile_of<BN>(p, plan, first_unit + li * unit_step);
-          row = (of_w ? t.wrow : t.row0) + lane;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < nj) v[j] = load_scales(src, row + 32 * j, nrows, per_row, (ks0 + lk) * (kK / 32));
-        if (++lk == kst) {
-          lk = 0;
-          ++li;
-        }
-      }
-    };
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) buf[q][j] = make_uint2(0u, 0u);
-      fetch(buf[q]);
-    }
+    const int atoms = of_w ? 1 : C::kAtoms;
+    Ring b;
     bool ok = true;
-    for (int g0 = 0; g0 < total && ok; g0 += kAhead) {
+    for (int i = 0; i < units && ok; ++i) {
+      const Tile t = tile_of<BN>(p, plan, first_unit + i * unit_step);
+      const uint8_t* src = of_w ? p.q.w_scales : p.q.x_scales;
+      const long long row = (of_w ? t.wrow : t.row0) + lane;
+      const long long nrows = of_w ? (long long)p.q.experts * p.q.N : p.q.rows;
+      for (int k = 0; k < blocks; ++k) {
+        uint8_t* slot = sf_ring + b.s * C::kSfSlot + (of_w ? 0 : 4 * kSfAtom);
+        uint4 v[2][4];
+        if (p.tma_scales) {
+          if (!(ok = wait_or_stop(&sf_raw[b.s], b.round, stop, p.q.flags))) break;
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q) {
-        const int g = g0 + q;
-        if (g < total && ok) {
-          const int s = g % kS;
-          if (g >= kS)
-            ok = warp_wait_or_stop(&empty[s], (uint32_t)((g / kS - 1) & 1), stop, p.q.flags);
-          if (ok) {
-            uint8_t* dst = sf_tile(s) + (of_w ? 0 : 2 * kSfAtom) + lane * 16;
-            *reinterpret_cast<uint4*>(dst) = make_uint4(buf[q][0].x, buf[q][1].x, buf[q][2].x, buf[q][3].x);
-            *reinterpret_cast<uint4*>(dst + kSfAtom) =
-                make_uint4(buf[q][0].y, buf[q][1].y, buf[q][2].y, buf[q][3].y);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
-            fetch(buf[q]);
-          }
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (h < atoms)
+                v[h][j] = *reinterpret_cast<const uint4*>(slot + (h * 128 + j * 32 + lane) * 16);
+          __syncwarp();
+        } else {
+          const int at = (k0 + k * kBlockK) / 32;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (h < atoms)
+                v[h][j] = (of_w || h * 128 + j * 32 < BN)
+                              ? load_scales(src, row + h * 128 + j * 32, nrows, p.q.K / 32, at)
+                              : make_uint4(0u, 0u, 0u, 0u);
+          if (!(ok = wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags))) break;
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (h < atoms) {
+            uint8_t* dst = slot + h * kSfAtom + lane * 16;
+            const int step = atoms * kSfAtom;
+            *reinterpret_cast<uint4*>(dst) = make_uint4(v[h][0].x, v[h][1].x, v[h][2].x, v[h][3].x);
+            *reinterpret_cast<uint4*>(dst + step) =
+                make_uint4(v[h][0].y, v[h][1].y, v[h][2].y, v[h][3].y);
+            *reinterpret_cast<uint4*>(dst + 2 * step) =
+                make_uint4(v[h][0].z, v[h][1].z, v[h][2].z, v[h][3].z);
+            *reinterpret_cast<uint4*>(dst + 3 * step) =
+                make_uint4(v[h][0].w, v[h][1].w, v[h][2].w, v[h][3].w);
+          }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sf_full[b.s]);
+        b.next<kSfSlots>();
       }
     }
-  } else if (splits == 1) {
-    // epilogue: lane = feature, column = row of x
+  } else {
+    // ---- epilogue: lane = feature, column = row of x ----
     const int quarter = warp & 3;
+    const int c_first = ((warp - 4) >> 2) * C::kWarpCols;
     OT* y = reinterpret_cast<OT*>(p.q.y);
+    Ring acc;
     for (int i = 0; i < units; ++i) {
       const Tile t = tile_of<BN>(p, plan, first_unit + i * unit_step);
-      const int acc = i & 1;
-      if (!warp_wait_or_stop(&accfull[acc], (uint32_t)((i / 2) & 1), stop, p.q.flags)) break;
+      if (!wait_or_stop(&accfull[acc.s], acc.round, stop, p.q.flags)) break;
+      __syncwarp();
       tc_fence_after();
       const int f = t.f0 + quarter * 32 + lane;
       const bool f_ok = f < p.q.N;
+      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc.s * BN + c_first);
+      if (sizeof(OT) == 2) {
+        // all of it into registers first, so that the accumulator is free early
+        uint32_t h[C::kWarpCols / 32][16];
 #pragma unroll
-      for (int c0 = 0; c0 < BN; c0 += 32) {
-        if (c0 < t.rows) {   // warp-uniform
-          float v[32];
-          tmem_ld_32x32(tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * BN + c0), v);
-          if (f_ok) {
-            OT* o = y + (size_t)(t.row0 + c0) * p.q.N + f;
+        for (int c = 0; c < C::kWarpCols / 32; ++c)
+          if (c_first + c * 32 < t.rows) {   // warp-uniform
+            float v[32];
+            tmem_ld_32x32(src + c * 32, v);
 #pragma unroll
-            for (int n = 0; n < 32; ++n)
-              if (c0 + n < t.rows) o[(size_t)n * p.q.N] = from_f32<OT>(v[n]);
+            for (int n = 0; n < 16; ++n) h[c][n] = pack2_any(OT(), v[2 * n], v[2 * n + 1]);
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&accempty[acc.s]);
+#pragma unroll
+        for (int c = 0; c < C::kWarpCols / 32; ++c) {
+          const int c0 = c_first + c * 32;
+          if (c0 < t.rows)
+            store_columns(y + (size_t)(t.row0 + c0) * p.q.N, p.q.N, f, f_ok, t.rows - c0, h[c]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < C::kWarpCols / 32; ++c) {
+          const int c0 = c_first + c * 32;
+          if (c0 < t.rows) {
+            float v[32];
+            tmem_ld_32x32(src + c * 32, v);
+            if (f_ok) {
+              float* o = reinterpret_cast<float*>(p.q.y) + (size_t)(t.row0 + c0) * p.q.N + f;
+#pragma unroll
+              for (int n = 0; n < 32; ++n)
+                if (c0 + n < t.rows) o[(size_t)n * p.q.N] = v[n];
+            }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&accempty[acc.s]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&accempty[acc]);
+      acc.next<C::kAcc>();
     }
   }
 
@@ -408,9 +537,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Tensor map over `rows` rows of `bytes` bytes, box 128 bytes x box_rows.
+// Tensor map over `rows` rows of `bytes` bytes, box box_bytes x box_rows.
 cudaError_t make_map(CUtensorMap* map, const void* ptr, uint64_t bytes, uint64_t rows,
-                     uint32_t box_rows, const char** why) {
+                     uint32_t box_bytes, uint32_t box_rows, const char** why) {
   auto fn = encode_fn();
   if (fn == nullptr) {
     *why = "cuTensorMapEncodeTiled is not available";
@@ -418,10 +547,11 @@ cudaError_t make_map(CUtensorMap* map, const void* ptr, uint64_t bytes, uint64_t
   }
   const cuuint64_t dims[2] = {bytes, rows};
   const cuuint64_t strides[1] = {bytes};
-  const cuuint32_t box[2] = {kK / 2, box_rows};
+  const cuuint32_t box[2] = {box_bytes, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box,
-                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     *why = "cuTensorMapEncodeTiled rejected the tensor";
@@ -467,22 +597,30 @@ cudaError_t launch(const MxLinearParams& q, cudaStream_t stream, const char** wh
     }
   }
   const int experts = q.expert_offsets != nullptr ? q.experts : 1;
-  CUtensorMap map_w, map_x;
-  err = make_map(&map_w, q.w_codes, (uint64_t)q.K / 2, (uint64_t)experts * q.N, kM, why);
+  const uint64_t w_rows = (uint64_t)experts * q.N, x_rows = (uint64_t)q.rows;
+  CUtensorMap map_w, map_x, map_ws = {}, map_xs = {};
+  err = make_map(&map_w, q.w_codes, (uint64_t)q.K / 2, w_rows, kK / 2, kM, why);
   if (err != cudaSuccess) return err;
-  err = make_map(&map_x, q.x_codes, (uint64_t)q.K / 2, (uint64_t)q.rows, BN, why);
+  err = make_map(&map_x, q.x_codes, (uint64_t)q.K / 2, x_rows, kK / 2, BN, why);
   if (err != cudaSuccess) return err;
   Params p = {};
   p.q = q;
   p.ftiles = (q.N + kM - 1) / kM;
   p.splits = 1;
-  p.kstages = (q.K + kK - 1) / kK;
-  p.per_split = p.kstages;
+  p.blocks = (q.K + kBlockK - 1) / kBlockK;
+  p.per_split = p.blocks;
+  p.tma_scales = q.K % kBlockK == 0;
+  if (p.tma_scales) {
+    err = make_map(&map_ws, q.w_scales, (uint64_t)q.K / 32, w_rows, kBlockK / 32, kM, why);
+    if (err != cudaSuccess) return err;
+    err = make_map(&map_xs, q.x_scales, (uint64_t)q.K / 32, x_rows, kBlockK / 32, BN, why);
+    if (err != cudaSuccess) return err;
+  }
   // tiles there can be: every expert's last one may be partial
   const long long bound =
       ((long long)(q.rows + BN - 1) / BN + (experts > 1 ? min(experts, q.rows) : 0)) * p.ftiles;
   const int grid = (int)min((long long)sms, bound);
-  mx_linear_kernel<BN, OT><<<grid, kThreads, C::kSmem, stream>>>(map_w, map_x, p);
+  mx_linear_kernel<BN, OT><<<grid, C::kThreads, C::kSmem, stream>>>(map_w, map_x, map_ws, map_xs, p);
   return cudaGetLastError();
 }
 
@@ -493,7 +631,8 @@ cudaError_t launch_typed(const MxLinearParams& q, cudaStream_t stream, const cha
   if (mean <= 16) return launch<16, OT>(q, stream, why);
   if (mean <= 32) return launch<32, OT>(q, stream, why);
   if (mean <= 64) return launch<64, OT>(q, stream, why);
-  return launch<128, OT>(q, stream, why);
+  if (mean <= 128) return launch<128, OT>(q, stream, why);
+  return launch<256, OT>(q, stream, why);
 }
 
 }  // namespace

@@ -244,11 +244,13 @@ def lora_expert_apply(x_sorted, y_sorted, a, b, pair_index, ranks, scalings, row
 _TYPES = (LORA_TYPE_BF16, LORA_TYPE_F16, LORA_TYPE_F32)
 _torch = None      # the torch module and its element types, once a tensor is given
 _dtypes = None
+_raw_stream = None
 
 
 def _import_torch():
-    global _torch, _dtypes
+    global _torch, _dtypes, _raw_stream
     import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _dtypes = {LORA_TYPE_BF16: torch.bfloat16, LORA_TYPE_F16: torch.float16,
                LORA_TYPE_F32: torch.float32, "int32": torch.int32, "uint8": torch.uint8}
     _torch = torch
@@ -297,7 +299,11 @@ def _call(fn, dev, stream, *args):
             _check(fn(*args, _torch.cuda.current_stream().cuda_stream if stream is None
                       else stream))
         return
-    status = fn(*args, _stream(None) if stream is None else stream)
+    if stream is None:
+        # the raw handle: torch.cuda.current_stream() builds an object around it,
+        # which costs more than the rest of a call
+        stream = _raw_stream(dev) if _raw_stream is not None and dev is not None else _stream(None)
+    status = fn(*args, stream)
     if status != LORA_OK:
         _check(status)
 
