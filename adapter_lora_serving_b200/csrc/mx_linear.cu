@@ -44,6 +44,7 @@ constexpr int kATile = kM * kK / 2;   // 16 KB
 constexpr int kBlockK = 512;          // elements of k per block of scales (16 bytes a row)
 constexpr int kSfAtom = 512;          // scales of 128 rows x 128 elements
 constexpr int kSfSlots = 3;           // blocks of scales in flight
+constexpr int kTurn = 1024;            // an epilogue warp's 16 rows x 32 features of 16 bits
 constexpr int kHeader = 6144;         // barriers, scan scratch and the experts' tile prefix (1025 ints)
 
 template <int BN>
@@ -54,7 +55,6 @@ struct Cfg {
   static constexpr int kAtoms = BN > 128 ? 2 : 1;             // of x, per 128 elements of k
   static constexpr int kSfX = 4 * kAtoms * kSfAtom;
   static constexpr int kSfSlot = 4 * kSfAtom + kSfX;
-  static constexpr int kSmem = 1024 + kHeader + kStages * kStage + kSfSlots * kSfSlot;   // 1024: alignment slack
   static constexpr int kAcc = BN > 128 ? 1 : 2;               // accumulators
   static constexpr int kSfCols = 16 + 16 * kAtoms;            // tensor memory columns of a block of scales
   static constexpr int kUsed = kAcc * BN + 2 * kSfCols;
@@ -62,6 +62,8 @@ struct Cfg {
   static constexpr int kEpiWarps = BN >= 64 ? 8 : 4;
   static constexpr int kWarpCols = BN >= 64 ? BN / 2 : 32;    // columns an epilogue warp drains
   static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  static constexpr int kSmem = 1024 + kHeader + kStages * kStage + kSfSlots * kSfSlot +
+                               kEpiWarps * kTurn;   // 1024: alignment slack
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -215,20 +217,84 @@ LORA_DEV uint4 load_scales(const uint8_t* base, long long row, long long rows, i
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A thread's 32 columns of its feature, tokens [0, rows), to y.  16-bit types:
-// neighbouring lanes trade halves, so that each stores two features at once.
-template <typename OT>
-LORA_DEV void store_columns(OT* y, int N, int f, bool f_ok, int rows, const uint32_t (&v)[16]) {
+// Rows' 16 scale bytes into atoms: word c of row 32 j + l becomes word j of lane
+// l of atom c.  Whole warp; visible to the tensor core's copies on return.
+template <int A>
+LORA_DEV void write_scales(uint8_t* slot, const uint4 (&v)[A][4], int atoms) {
   const int lane = threadIdx.x & 31;
-  const bool odd = lane & 1;
-  // N is a multiple of 8, so a feature and its neighbour are valid together
-  OT* o = y + (f - (odd ? 1 : 0)) + (odd ? (size_t)N : (size_t)0);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, v[i], 1);
-    const uint32_t out = odd ? __byte_perm(other, v[i], 0x7632) : __byte_perm(v[i], other, 0x5410);
-    if (f_ok && 2 * i + (odd ? 1 : 0) < rows)
-      *reinterpret_cast<uint32_t*>(o + (size_t)(2 * i) * N) = out;
+  for (int h = 0; h < A; ++h)
+    if (h < atoms) {
+      uint8_t* dst = slot + h * kSfAtom + lane * 16;
+      const int step = atoms * kSfAtom;
+      *reinterpret_cast<uint4*>(dst) = make_uint4(v[h][0].x, v[h][1].x, v[h][2].x, v[h][3].x);
+      *reinterpret_cast<uint4*>(dst + step) = make_uint4(v[h][0].y, v[h][1].y, v[h][2].y, v[h][3].y);
+      *reinterpret_cast<uint4*>(dst + 2 * step) =
+          make_uint4(v[h][0].z, v[h][1].z, v[h][2].z, v[h][3].z);
+      *reinterpret_cast<uint4*>(dst + 3 * step) =
+          make_uint4(v[h][0].w, v[h][1].w, v[h][2].w, v[h][3].w);
+    }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// 16 lanes x 32 columns of fp32 from tensor memory in the layout of a matrix
+// fragment: of each 8 columns the thread gets lanes l / 4 and l / 4 + 8, columns
+// 2 (l % 4) and the next.  Packed in pairs of columns: out[2 c8 + half].
+template <typename OT>
+LORA_DEV void tmem_ld_fragments(uint32_t taddr, uint32_t (&out)[8]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    out[i] = pack2_any(OT(), __uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+
+LORA_DEV void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// A warp's 32 features x 32 columns (lo: features 0..15, hi: 16..31, as above)
+// to y, `rows` of the columns being rows of y.  Turned in shared memory, 16 rows
+// at a time, to 64 bytes of features a row (16-byte chunks swizzled by the row),
+// then stored 16 bytes a lane.
+template <typename OT>
+LORA_DEV void store_fragments(OT* y, int N, int f0, int rows, uint8_t* turn, const uint32_t (&lo)[8],
+                              const uint32_t (&hi)[8]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = smem_u32(turn);
+  // stmatrix: lanes 8 i .. 8 i + 7 address the rows of matrix i: features 8 i..
+  const int r8 = lane & 7, q = lane >> 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (16 * h >= rows) break;
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = 8 * c + r8;
+      const int i = 2 * (2 * h + c);
+      stmatrix_x4_trans(base + row * 64 + ((q ^ ((row >> 1) & 3)) << 4), lo[i], lo[i + 1], hi[i],
+                        hi[i + 1]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int row = 8 * c + (lane >> 2), ch = lane & 3;
+      const uint4 v =
+          *reinterpret_cast<const uint4*>(turn + row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+      if (16 * h + row < rows && f0 + ch * 8 < N)
+        *reinterpret_cast<uint4*>(y + (size_t)(16 * h + row) * N + f0 + ch * 8) = v;
+    }
   }
 }
 
@@ -243,8 +309,9 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   uint8_t* base = mx_smem + (up1024(smem_u32(mx_smem)) - smem_u32(mx_smem));
   uint64_t* full = reinterpret_cast<uint64_t*>(base);
   uint64_t* empty = full + kS;
-  uint64_t* sf_raw = empty + kS;            // a block of scales has landed (by TMA)
-  uint64_t* sf_full = sf_raw + kSfSlots;    // ... is in order
+  uint64_t* sf_raw = empty + kS;                // a block of scales has landed (by TMA):
+                                                // the weight's, then x's
+  uint64_t* sf_full = sf_raw + 2 * kSfSlots;    // ... is in order
   uint64_t* sf_empty = sf_full + kSfSlots;  // ... is in tensor memory
   uint64_t* accfull = sf_empty + kSfSlots;
   uint64_t* accempty = accfull + 2;
@@ -254,6 +321,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   int* prefix = reinterpret_cast<int*>(base + 1024);   // up to 1025 ints
   uint8_t* ring = base + kHeader;
   uint8_t* sf_ring = ring + kS * C::kStage;
+  uint8_t* turn = sf_ring + kSfSlots * C::kSfSlot;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = p.splits;
@@ -273,6 +341,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     }
     for (int i = 0; i < kSfSlots; ++i) {
       mbar_init(&sf_raw[i], 1);
+      mbar_init(&sf_raw[kSfSlots + i], 1);
       mbar_init(&sf_full[i], 2);    // the two scale warps
       mbar_init(&sf_empty[i], 1);
     }
@@ -321,21 +390,12 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   const int units = plan.tiles > first_unit ? (plan.tiles - first_unit - 1) / unit_step + 1 : 0;
 
   if (warp == 0) {
-    // ---- element tiles and raw scales ----
+    // ---- element tiles ----
     if (elect_one()) {
-      Ring r, b;
+      Ring r;
       for (int i = 0; i < units && !*stop; ++i) {
         const Tile t = tile_of<BN>(p, plan, first_unit + i * unit_step);
         for (int k = 0; k < stages; ++k) {
-          if ((k & 1) == 0 && p.tma_scales) {
-            if (!wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags)) break;
-            uint8_t* slot = sf_ring + b.s * C::kSfSlot;
-            const int at = (k0 + k * kK) / 32;
-            mbar_arrive_expect_tx(&sf_raw[b.s], (kM + BN) * 16);
-            tma_load_2d(slot, &map_ws, at, t.wrow, &sf_raw[b.s]);
-            tma_load_2d(slot + 4 * kSfAtom, &map_xs, at, t.row0, &sf_raw[b.s]);
-            b.next<kSfSlots>();
-          }
           if (!wait_or_stop(&empty[r.s], r.round ^ 1u, stop, p.q.flags)) break;
           uint8_t* slot = ring + r.s * C::kStage;
           const int at = (k0 + k * kK) / 2;
@@ -401,54 +461,87 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     // 16 bytes are one word for each of four atoms. ----
     const bool of_w = warp == 2;
     const int atoms = of_w ? 1 : C::kAtoms;
+    const int total = units * blocks;
+    uint8_t* ring_of = sf_ring + (of_w ? 0 : 4 * kSfAtom);
+    uint64_t* raw = sf_raw + (of_w ? 0 : kSfSlots);
+    // the next block to fetch: its unit, block and first row
+    int nu = 0, nb = 0, row0 = 0;
+    Ring fr;
+    auto step = [&]() {
+      if (nb == 0) {
+        const Tile t = tile_of<BN>(p, plan, first_unit + nu * unit_step);
+        row0 = of_w ? t.wrow : t.row0;
+      }
+    };
+    auto stepped = [&]() {
+      if (++nb == blocks) {
+        nb = 0;
+        ++nu;
+      }
+    };
     Ring b;
     bool ok = true;
-    for (int i = 0; i < units && ok; ++i) {
-      const Tile t = tile_of<BN>(p, plan, first_unit + i * unit_step);
-      const uint8_t* src = of_w ? p.q.w_scales : p.q.x_scales;
-      const long long row = (of_w ? t.wrow : t.row0) + lane;
-      const long long nrows = of_w ? (long long)p.q.experts * p.q.N : p.q.rows;
-      for (int k = 0; k < blocks; ++k) {
-        uint8_t* slot = sf_ring + b.s * C::kSfSlot + (of_w ? 0 : 4 * kSfAtom);
-        uint4 v[2][4];
-        if (p.tma_scales) {
-          if (!(ok = wait_or_stop(&sf_raw[b.s], b.round, stop, p.q.flags))) break;
+    if (p.tma_scales) {
+      // lane 0 fetches ahead: block n + 2 once block n - 1 has left its slot
+      const int at0 = k0 / 32;
+      auto fetch = [&]() {
+        step();
+        if (!wait_or_stop(&sf_empty[fr.s], fr.round ^ 1u, stop, p.q.flags)) return false;
+        mbar_arrive_expect_tx(&raw[fr.s], (of_w ? kM : BN) * 16);
+        tma_load_2d(ring_of + fr.s * C::kSfSlot, of_w ? &map_ws : &map_xs, at0 + nb * (kBlockK / 32),
+                    row0, &raw[fr.s]);
+        fr.next<kSfSlots>();
+        stepped();
+        return true;
+      };
+      if (lane == 0)
+        for (int n = 0; n < 2 && n < total; ++n) ok = ok && fetch();
+      for (int n = 0; n < total; ++n) {
+        if (lane == 0 && ok && n + 2 < total) ok = fetch();
+        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+        uint8_t* slot = ring_of + b.s * C::kSfSlot;
+        ok = wait_or_stop(&raw[b.s], b.round, stop, p.q.flags);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        uint4 v[C::kAtoms][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < C::kAtoms; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (h < atoms)
-                v[h][j] = *reinterpret_cast<const uint4*>(slot + (h * 128 + j * 32 + lane) * 16);
-          __syncwarp();
-        } else {
-          const int at = (k0 + k * kBlockK) / 32;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (h < atoms)
-                v[h][j] = (of_w || h * 128 + j * 32 < BN)
-                              ? load_scales(src, row + h * 128 + j * 32, nrows, p.q.K / 32, at)
-                              : make_uint4(0u, 0u, 0u, 0u);
-          if (!(ok = wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags))) break;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (h < atoms) {
-            uint8_t* dst = slot + h * kSfAtom + lane * 16;
-            const int step = atoms * kSfAtom;
-            *reinterpret_cast<uint4*>(dst) = make_uint4(v[h][0].x, v[h][1].x, v[h][2].x, v[h][3].x);
-            *reinterpret_cast<uint4*>(dst + step) =
-                make_uint4(v[h][0].y, v[h][1].y, v[h][2].y, v[h][3].y);
-            *reinterpret_cast<uint4*>(dst + 2 * step) =
-                make_uint4(v[h][0].z, v[h][1].z, v[h][2].z, v[h][3].z);
-            *reinterpret_cast<uint4*>(dst + 3 * step) =
-                make_uint4(v[h][0].w, v[h][1].w, v[h][2].w, v[h][3].w);
-          }
-        fence_proxy_async_smem();
+          for (int j = 0; j < 4; ++j)
+            if (h < atoms)
+              v[h][j] = *reinterpret_cast<const uint4*>(slot + (h * 128 + j * 32 + lane) * 16);
         __syncwarp();
+        write_scales<C::kAtoms>(slot, v, atoms);
         if (lane == 0) mbar_arrive(&sf_full[b.s]);
         b.next<kSfSlots>();
+      }
+    } else {
+      // rows of any multiple of one byte: loaded a block ahead
+      const uint8_t* src = of_w ? p.q.w_scales : p.q.x_scales;
+      const long long nrows = of_w ? (long long)p.q.experts * p.q.N : p.q.rows;
+      const int rows_of = of_w ? kM : BN;
+      uint4 v[C::kAtoms][4];
+      auto fetch = [&]() {
+        step();
+#pragma unroll
+        for (int h = 0; h < C::kAtoms; ++h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = h * 128 + j * 32;
+            v[h][j] = h < atoms && r < rows_of
+                          ? load_scales(src, (long long)row0 + lane + r, nrows, p.q.K / 32,
+                                        (k0 + nb * kBlockK) / 32)
+                          : make_uint4(0u, 0u, 0u, 0u);
+          }
+        stepped();
+      };
+      if (total > 0) fetch();
+      for (int n = 0; n < total; ++n) {
+        ok = wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        write_scales<C::kAtoms>(ring_of + b.s * C::kSfSlot, v, atoms);
+        if (lane == 0) mbar_arrive(&sf_full[b.s]);
+        b.next<kSfSlots>();
+        if (n + 1 < total) fetch();
       }
     }
   } else {
@@ -467,14 +560,12 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc.s * BN + c_first);
       if (sizeof(OT) == 2) {
         // all of it into registers first, so that the accumulator is free early
-        uint32_t h[C::kWarpCols / 32][16];
+        uint32_t lo[C::kWarpCols / 32][8], hi[C::kWarpCols / 32][8];
 #pragma unroll
         for (int c = 0; c < C::kWarpCols / 32; ++c)
           if (c_first + c * 32 < t.rows) {   // warp-uniform
-            float v[32];
-            tmem_ld_32x32(src + c * 32, v);
-#pragma unroll
-            for (int n = 0; n < 16; ++n) h[c][n] = pack2_any(OT(), v[2 * n], v[2 * n + 1]);
+            tmem_ld_fragments<OT>(src + c * 32, lo[c]);
+            tmem_ld_fragments<OT>(src + (16u << 16) + c * 32, hi[c]);
           }
         tc_fence_before();
         __syncwarp();
@@ -483,7 +574,8 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         for (int c = 0; c < C::kWarpCols / 32; ++c) {
           const int c0 = c_first + c * 32;
           if (c0 < t.rows)
-            store_columns(y + (size_t)(t.row0 + c0) * p.q.N, p.q.N, f, f_ok, t.rows - c0, h[c]);
+            store_fragments(y + (size_t)(t.row0 + c0) * p.q.N, p.q.N, t.f0 + quarter * 32,
+                            t.rows - c0, turn + (warp - 4) * kTurn, lo[c], hi[c]);
         }
       } else {
 #pragma unroll
