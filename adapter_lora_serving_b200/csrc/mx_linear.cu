@@ -61,7 +61,7 @@ struct Cfg {
   static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static constexpr int kEpiWarps = BN >= 64 ? 8 : 4;
   static constexpr int kWarpCols = BN >= 64 ? BN / 2 : 32;    // columns an epilogue warp drains
-  static constexpr int kThreads = 128 + 32 * kEpiWarps;
+  static constexpr int kThreads = 160 + 32 * kEpiWarps;       // and the scales' producer
   static constexpr int kSmem = 1024 + kHeader + kStages * kStage + kSfSlots * kSfSlot +
                                kEpiWarps * kTurn;   // 1024: alignment slack
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -217,25 +217,66 @@ LORA_DEV uint4 load_scales(const uint8_t* base, long long row, long long rows, i
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Rows' 16 scale bytes into atoms: word c of row 32 j + l becomes word j of lane
-// l of atom c.  Whole warp; visible to the tensor core's copies on return.
-template <int A>
-LORA_DEV void write_scales(uint8_t* slot, const uint4 (&v)[A][4], int atoms) {
+// Scales of a tile's ROWS rows into the order the tensor core reads, block after
+// block (the whole warp): lane l has rows l, l + 32, l + 64, l + 96 of an atom; word
+// c of row 32 j + l becomes word j of lane l of atom c.  Raw rows are in the slot
+// already (by TMA, in place), or are loaded here, a block ahead.
+template <int ATOMS, int ROWS, typename RowOf>
+LORA_DEV void order_scales(const Params& p, uint8_t* ring, int slot_bytes, uint64_t* raw,
+                           uint64_t* ready, uint64_t* empty, volatile int* stop, int total,
+                           RowOf row_of, const uint8_t* src, long long nrows, int k0, int blocks) {
   const int lane = threadIdx.x & 31;
+  uint4 v[ATOMS][4];
+  Ring b;
+  int unit = 0, block = 0;
+  long long row = 0;
+  auto load = [&]() {
+    if (block == 0) row = (long long)row_of(unit) + lane;
 #pragma unroll
-  for (int h = 0; h < A; ++h)
-    if (h < atoms) {
-      uint8_t* dst = slot + h * kSfAtom + lane * 16;
-      const int step = atoms * kSfAtom;
+    for (int h = 0; h < ATOMS; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[h][j] = h * 128 + j * 32 < ROWS
+                      ? load_scales(src, row + h * 128 + j * 32, nrows, p.q.K / 32,
+                                    (k0 + block * kBlockK) / 32)
+                      : make_uint4(0u, 0u, 0u, 0u);
+    if (++block == blocks) {
+      block = 0;
+      ++unit;
+    }
+  };
+  const bool by_tma = p.tma_scales;
+  if (!by_tma && total > 0) load();
+  for (int n = 0; n < total; ++n) {
+    uint8_t* slot = ring + b.s * slot_bytes + lane * 16;
+    if (by_tma) {
+      if (!wait_or_stop(&raw[b.s], b.round, stop, p.q.flags)) break;
+#pragma unroll
+      for (int h = 0; h < ATOMS; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[h][j] = *reinterpret_cast<const uint4*>(slot + (h * 128 + j * 32) * 16);
+      __syncwarp();
+    } else {
+      if (!wait_or_stop(&empty[b.s], b.round ^ 1u, stop, p.q.flags)) break;
+    }
+#pragma unroll
+    for (int h = 0; h < ATOMS; ++h) {
+      uint8_t* dst = slot + h * kSfAtom;
+      constexpr int kStep = ATOMS * kSfAtom;
       *reinterpret_cast<uint4*>(dst) = make_uint4(v[h][0].x, v[h][1].x, v[h][2].x, v[h][3].x);
-      *reinterpret_cast<uint4*>(dst + step) = make_uint4(v[h][0].y, v[h][1].y, v[h][2].y, v[h][3].y);
-      *reinterpret_cast<uint4*>(dst + 2 * step) =
+      *reinterpret_cast<uint4*>(dst + kStep) = make_uint4(v[h][0].y, v[h][1].y, v[h][2].y, v[h][3].y);
+      *reinterpret_cast<uint4*>(dst + 2 * kStep) =
           make_uint4(v[h][0].z, v[h][1].z, v[h][2].z, v[h][3].z);
-      *reinterpret_cast<uint4*>(dst + 3 * step) =
+      *reinterpret_cast<uint4*>(dst + 3 * kStep) =
           make_uint4(v[h][0].w, v[h][1].w, v[h][2].w, v[h][3].w);
     }
-  fence_proxy_async_smem();
-  __syncwarp();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ready[b.s]);
+    b.next<kSfSlots>();
+    if (!by_tma && n + 1 < total) load();
+  }
 }
 
 // 16 lanes x 32 columns of fp32 from tensor memory in the layout of a matrix
@@ -459,89 +500,32 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     // ---- scales into the tensor core's order: warp 2 the weight's 128 rows, warp
     // 3 those of x.  Lane l has rows l, l + 32, l + 64, l + 96 of an atom; a row's
     // 16 bytes are one word for each of four atoms. ----
-    const bool of_w = warp == 2;
-    const int atoms = of_w ? 1 : C::kAtoms;
-    const int total = units * blocks;
-    uint8_t* ring_of = sf_ring + (of_w ? 0 : 4 * kSfAtom);
-    uint64_t* raw = sf_raw + (of_w ? 0 : kSfSlots);
-    // the next block to fetch: its unit, block and first row
-    int nu = 0, nb = 0, row0 = 0;
-    Ring fr;
-    auto step = [&]() {
-      if (nb == 0) {
-        const Tile t = tile_of<BN>(p, plan, first_unit + nu * unit_step);
-        row0 = of_w ? t.wrow : t.row0;
-      }
-    };
-    auto stepped = [&]() {
-      if (++nb == blocks) {
-        nb = 0;
-        ++nu;
-      }
-    };
-    Ring b;
-    bool ok = true;
-    if (p.tma_scales) {
-      // lane 0 fetches ahead: block n + 2 once block n - 1 has left its slot
-      const int at0 = k0 / 32;
-      auto fetch = [&]() {
-        step();
-        if (!wait_or_stop(&sf_empty[fr.s], fr.round ^ 1u, stop, p.q.flags)) return false;
-        mbar_arrive_expect_tx(&raw[fr.s], (of_w ? kM : BN) * 16);
-        tma_load_2d(ring_of + fr.s * C::kSfSlot, of_w ? &map_ws : &map_xs, at0 + nb * (kBlockK / 32),
-                    row0, &raw[fr.s]);
-        fr.next<kSfSlots>();
-        stepped();
-        return true;
-      };
-      if (lane == 0)
-        for (int n = 0; n < 2 && n < total; ++n) ok = ok && fetch();
-      for (int n = 0; n < total; ++n) {
-        if (lane == 0 && ok && n + 2 < total) ok = fetch();
-        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-        uint8_t* slot = ring_of + b.s * C::kSfSlot;
-        ok = wait_or_stop(&raw[b.s], b.round, stop, p.q.flags);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        uint4 v[C::kAtoms][4];
-#pragma unroll
-        for (int h = 0; h < C::kAtoms; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (h < atoms)
-              v[h][j] = *reinterpret_cast<const uint4*>(slot + (h * 128 + j * 32 + lane) * 16);
-        __syncwarp();
-        write_scales<C::kAtoms>(slot, v, atoms);
-        if (lane == 0) mbar_arrive(&sf_full[b.s]);
-        b.next<kSfSlots>();
-      }
-    } else {
-      // rows of any multiple of one byte: loaded a block ahead
-      const uint8_t* src = of_w ? p.q.w_scales : p.q.x_scales;
-      const long long nrows = of_w ? (long long)p.q.experts * p.q.N : p.q.rows;
-      const int rows_of = of_w ? kM : BN;
-      uint4 v[C::kAtoms][4];
-      auto fetch = [&]() {
-        step();
-#pragma unroll
-        for (int h = 0; h < C::kAtoms; ++h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = h * 128 + j * 32;
-            v[h][j] = h < atoms && r < rows_of
-                          ? load_scales(src, (long long)row0 + lane + r, nrows, p.q.K / 32,
-                                        (k0 + nb * kBlockK) / 32)
-                          : make_uint4(0u, 0u, 0u, 0u);
-          }
-        stepped();
-      };
-      if (total > 0) fetch();
-      for (int n = 0; n < total; ++n) {
-        ok = wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        write_scales<C::kAtoms>(ring_of + b.s * C::kSfSlot, v, atoms);
-        if (lane == 0) mbar_arrive(&sf_full[b.s]);
-        b.next<kSfSlots>();
-        if (n + 1 < total) fetch();
+    if (warp == 2)
+      order_scales<1, kM>(p, sf_ring, C::kSfSlot, sf_raw, sf_full, sf_empty, stop, units * blocks,
+                          [&](int i) { return tile_of<BN>(p, plan, first_unit + i * unit_step).wrow; },
+                          p.q.w_scales, (long long)p.q.experts * p.q.N, k0, blocks);
+    else
+      order_scales<C::kAtoms, BN>(p, sf_ring + 4 * kSfAtom, C::kSfSlot, sf_raw + kSfSlots, sf_full,
+                                  sf_empty, stop, units * blocks,
+                                  [&](int i) { return tile_of<BN>(p, plan, first_unit + i * unit_step).row0; },
+                                  p.q.x_scales, p.q.rows, k0, blocks);
+  } else if (warp == 4 + C::kEpiWarps) {
+    // ---- raw scales, where they come by TMA ----
+    if (p.tma_scales && elect_one()) {
+      Ring b;
+      bool ok = true;
+      for (int i = 0; i < units && ok; ++i) {
+        const Tile t = tile_of<BN>(p, plan, first_unit + i * unit_step);
+        for (int k = 0; k < blocks; ++k) {
+          if (!(ok = wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags))) break;
+          uint8_t* slot = sf_ring + b.s * C::kSfSlot;
+          const int at = k0 / 32 + k * (kBlockK / 32);
+          mbar_arrive_expect_tx(&sf_raw[b.s], kM * 16);
+          tma_load_2d(slot, &map_ws, at, t.wrow, &sf_raw[b.s]);
+          mbar_arrive_expect_tx(&sf_raw[kSfSlots + b.s], BN * 16);
+          tma_load_2d(slot + 4 * kSfAtom, &map_xs, at, t.row0, &sf_raw[kSfSlots + b.s]);
+          b.next<kSfSlots>();
+        }
       }
     }
   } else {
