@@ -95,13 +95,20 @@ LORA_DEV void load_row(const LT* row, int lane, int E, float (&x)[VPL], bool* ba
     }
 }
 
+// e^z and a / b: in 64 bits, or for fp32 keys whose error is accounted for (Within)
+// the fast ones: 2 + 1.173 |z| ulps and 2 ulps.
+LORA_DEV double power(double z) { return exp(z); }
+LORA_DEV float power(float z) { return __expf(z); }
+LORA_DEV double quotient(double a, double b) { return a / b; }
+LORA_DEV float quotient(float a, float b) { return __fdividef(a, b); }
+
 // Scores s of the lane's experts and their selection keys s + bias, in V.
 // Returns the largest score of the row.
 template <int VPL, typename V>
 LORA_DEV V scores(const RouteParams& p, int lane, const float (&x)[VPL], V (&s)[VPL]) {
   if (p.score == LORA_SCORE_SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = (V)1 / ((V)1 + exp(-(V)x[i]));
+    for (int i = 0; i < VPL; ++i) s[i] = quotient((V)1, (V)1 + power(-(V)x[i]));
     return (V)1;
   }
   float m = -INFINITY;
@@ -114,7 +121,7 @@ LORA_DEV V scores(const RouteParams& p, int lane, const float (&x)[VPL], V (&s)[
   V sum = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    s[i] = exp((V)x[i] - (V)m);
+    s[i] = power((V)x[i] - (V)m);
     sum += s[i];
   }
 #pragma unroll
@@ -123,6 +130,38 @@ LORA_DEV V scores(const RouteParams& p, int lane, const float (&x)[VPL], V (&s)[
 #pragma unroll
   for (int i = 0; i < VPL; ++i) s[i] = s[i] * inv;
   return inv;   // the largest: exp(0) / sum
+}
+
+struct Exact {
+  static constexpr bool kExact = true;
+  template <typename V>
+  LORA_DEV V operator()(V) const { return (V)-1; }
+  LORA_DEV float of_sum(uint32_t) const { return -1.0f; }
+};
+LORA_DEV uint32_t magnitude_of(double) { return 0; }   // (kExact only)
+// Twice the error of an fp32 key, in units of u = 2^-23.
+//   sigmoid: e^-x moves the score by s (1 - s) (2 + 1.173 |x|) u < u (|x| s (1 - s)
+//     < .23); the sum and the quotient by 3 s u: 4 u of the largest score, 1.
+//   softmax: a term e^z by s (2 + 1.173 |z|) u <= 2.5 u smax (z e^z < .37); the
+//     sum by 2.5 u and half a u for each of VPL + 5 additions, the quotient and the
+//     product by 2.5 u more: (8 + (VPL + 5) / 2) u smax.
+//   the bias sum: half a u of the key; the place within the lane that fills its
+//     lowest bits (SortedKeys): 8 u at most of it.
+// A pair's sum has the errors of both its keys, whose magnitudes its own can be
+// far below: `of_sum` has the row's largest.
+struct Within {
+  static constexpr bool kExact = false;
+  float of_score;
+  LORA_DEV float operator()(float v) const { return of_score + 0x1p-18f * fabsf(v); }
+  LORA_DEV float of_sum(uint32_t magnitude) const {
+    return 2.0f * of_score + 0x1p-17f * __uint_as_float(warp_max(magnitude));
+  }
+};
+LORA_DEV uint32_t magnitude_of(float v) { return __float_as_uint(fabsf(v)); }
+template <int VPL>
+LORA_DEV Within key_error(float smax) {
+  Within w = {(float)(16 + VPL + 6) * 0x1p-23f * smax};
+  return w;
 }
 
 // Keeps the experts of the best top_groups groups (ties to the lowest group),
@@ -137,6 +176,7 @@ LORA_DEV bool keep_groups(const RouteParams& p, int lane, typename KeyOf<V>::U (
   const int n = p.E / p.num_groups;
   const bool pair = p.group_score == LORA_GROUP_TOP_PAIR;
   U mine = 0;   // this lane's group's score
+  uint32_t magnitude = 0;
   for (int g = 0; g < p.num_groups; ++g) {
     U a = 0, b = 0;   // the lane's two largest keys in group g
 #pragma unroll
@@ -156,6 +196,7 @@ LORA_DEV bool keep_groups(const RouteParams& p, int lane, typename KeyOf<V>::U (
       if (second != 0) score = order_of(value_of(top) + value_of(second));
     }
     if (lane == g) mine = score;
+    if (!Tol::kExact && a != 0) magnitude = max(magnitude, max(magnitude_of(value_of(a)), b != 0 ? magnitude_of(value_of(b)) : 0u));
   }
   // rank of this lane's group among all
   int rank = 0;
@@ -167,8 +208,11 @@ LORA_DEV bool keep_groups(const RouteParams& p, int lane, typename KeyOf<V>::U (
   const uint32_t keep = __ballot_sync(0xffffffffu, kept);
   const U worst_kept = ~warp_max(kept ? (U)~mine : (U)0);   // smallest kept score
   const U best_out = warp_max(lane < p.num_groups && !kept ? mine : (U)0);
-  const bool close = best_out != 0 && keep != 0 &&
-                     value_of(worst_kept) - value_of(best_out) <= tol(value_of(worst_kept));
+  bool close = false;
+  if (!Tol::kExact) {
+    const float border = tol.of_sum(magnitude);
+    close = best_out != 0 && keep != 0 && value_of(worst_kept) - value_of(best_out) <= border;
+  }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane * VPL + i;
@@ -217,20 +261,6 @@ LORA_DEV int take_best(const RouteParams& p, int lane, typename KeyOf<V>::U (&u)
   return id;
 }
 
-struct Exact {
-  static constexpr bool kExact = true;
-  template <typename V>
-  LORA_DEV V operator()(V) const { return (V)-1; }
-};
-// Twice the error of an fp32 key: the score's (expf and a division within 8
-// ulps, the softmax sum within VPL + 5 more: 2^-18 of the row's largest score)
-// and the rounding of the bias sum.  A pair's sum has twice a key's.
-struct Within {
-  static constexpr bool kExact = false;
-  float of_score;
-  LORA_DEV float operator()(float v) const { return of_score + 0x1p-21f * fabsf(v); }
-};
-
 // Selection keys s + bias of the lane's experts; experts with a masked logit or
 // bias get key 0.
 template <int VPL, typename V>
@@ -244,6 +274,98 @@ LORA_DEV void make_keys(const RouteParams& p, int lane, const float (&x)[VPL],
     if (!(b < INFINITY)) *bad = true;
     u[i] = (x[i] > -INFINITY && b > -INFINITY && b < INFINITY) ? order_of(s[i] + (V)b) : 0;
   }
+}
+
+// A lane's keys (VPL <= 8) in descending order, for the fp32 selection whose close
+// calls are decided elsewhere, or on 16-bit logits: the lowest bits of a key hold
+// the expert's place (LB bits: 7 - i within the lane for approximate keys, 1023 - e
+// for 16-bit ones, which are exact and never tie then).  One sorting network, after
+// which a round of the selection looks at the lanes' first keys alone.
+template <int VPL>
+LORA_DEV void sort_keys(uint32_t (&u)[VPL]) {
+  auto order = [&](int i, int j) {
+    const uint32_t hi = max(u[i], u[j]);
+    u[j] = min(u[i], u[j]);
+    u[i] = hi;
+  };
+  if (VPL == 2) {
+    order(0, 1);
+  } else if (VPL == 4) {
+    order(0, 2); order(1, 3); order(0, 1); order(2, 3); order(1, 2);
+  } else if (VPL == 8) {
+    // Batcher's odd-even merge sort, 19 comparators
+    order(0, 1); order(2, 3); order(4, 5); order(6, 7);
+    order(0, 2); order(1, 3); order(4, 6); order(5, 7);
+    order(1, 2); order(5, 6);
+    order(0, 4); order(1, 5); order(2, 6); order(3, 7);
+    order(2, 4); order(3, 5);
+    order(1, 2); order(3, 4); order(5, 6);
+  }
+}
+
+// take_best on sorted keys.  kPlace: the keys carry the expert (1023 - e) and are
+// exact; else they carry 7 - i.
+template <int VPL, bool kPlace, typename Tol>
+LORA_DEV int take_sorted(const RouteParams& p, int lane, uint32_t (&u)[VPL], Tol tol, bool* close) {
+  int id = -1;
+  uint32_t prev = 0;
+  const int rounds = p.top_k + (kPlace ? 0 : 1);
+  for (int j = 0; j < rounds; ++j) {
+    const uint32_t m = warp_max(u[0]);
+    if (m == 0) break;
+    if (!kPlace) {
+      if (prev != 0 && value_of(prev) - value_of(m) <= tol(value_of(prev))) *close = true;
+      prev = m;
+      if (j == p.top_k) break;
+    }
+    const uint32_t holders = __ballot_sync(0xffffffffu, u[0] == m);
+    const int src = __ffs((int)holders) - 1;
+    if (lane == j) id = kPlace ? 1023 - (int)(m & 1023u) : src * VPL + 7 - (int)(m & 7u);
+    if (lane == src) {
+#pragma unroll
+      for (int i = 0; i + 1 < VPL; ++i) u[i] = u[i + 1];
+      u[VPL - 1] = 0;
+    }
+  }
+  return id;
+}
+
+// keep_groups on sorted keys, for groups of `span` whole lanes (a power of two).
+template <int VPL, typename Tol>
+LORA_DEV bool keep_sorted_groups(const RouteParams& p, int lane, int span, uint32_t (&u)[VPL],
+                                 Tol tol) {
+  const bool pair = p.group_score == LORA_GROUP_TOP_PAIR;
+  uint32_t a = u[0], b = VPL > 1 ? u[VPL > 1 ? 1 : 0] : 0u;
+  for (int o = 1; o < span; o <<= 1) {
+    const uint32_t c = __shfl_xor_sync(0xffffffffu, a, o), d = __shfl_xor_sync(0xffffffffu, b, o);
+    b = max(min(a, c), max(b, d));
+    a = max(a, c);
+  }
+  // every lane of a group has its score; equal scores rank by group
+  uint32_t score = a;
+  if (pair && b != 0) score = order_of(value_of(a) + value_of(b));
+  int rank = 0;
+  const int mine = lane / span;
+  for (int g = 0; g < p.num_groups; ++g) {
+    const uint32_t other = __shfl_sync(0xffffffffu, score, g * span);
+    rank += (other > score || (other == score && g < mine)) ? 1 : 0;
+  }
+  const bool real = mine < p.num_groups;
+  const bool kept = real && rank < p.top_groups;
+  bool close = false;
+  if (!Tol::kExact) {
+    const uint32_t worst_kept = ~warp_max(kept && score != 0 ? ~score : 0u);
+    const uint32_t best_out = warp_max(real && !kept ? score : 0u);
+    const uint32_t magnitude =
+        max(a != 0 ? magnitude_of(value_of(a)) : 0u, b != 0 ? magnitude_of(value_of(b)) : 0u);
+    const float border = tol.of_sum(magnitude);
+    close = best_out != 0 && value_of(worst_kept) - value_of(best_out) <= border;
+  }
+  if (!kept) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) u[i] = 0;
+  }
+  return close;
 }
 
 // The same selection in 64 bits, for the tokens whose fp32 keys come too close
@@ -281,24 +403,43 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
   const bool by_score = p.bias != nullptr || pair;
   int id;
   float inv_sum = 1.0f, row_max = 0.0f;   // softmax normalisation, where it is needed
+  // groups of whole lanes, a power of two of them
+  const int span = p.num_groups > 1 && p.E / p.num_groups % VPL == 0 ? p.E / p.num_groups / VPL : 0;
+  const bool lanes_fit = p.num_groups == 1 || (span > 0 && (span & (span - 1)) == 0);
   if (by_score) {
     float s[VPL];
     const float smax = scores<VPL, float>(p, lane, x, s);
     make_keys<VPL, float>(p, lane, x, s, u, &bad);
-    const Within tol = {0x1p-17f * smax};
+    const Within tol = key_error<VPL>(smax);
     bool close = false;
-    if (p.num_groups > 1) {
-      const Within tol2 = {0x1p-16f * smax};
-      close = keep_groups<VPL, float>(p, lane, u, tol2);
+    if (VPL <= 8 && lanes_fit) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (u[i] != 0) u[i] = (u[i] & ~7u) | (uint32_t)(7 - i);
+      sort_keys<VPL>(u);
+      if (p.num_groups > 1) close = keep_sorted_groups<VPL>(p, lane, span, u, tol);
+      id = take_sorted<VPL, false>(p, lane, u, tol, &close);
+    } else {
+      if (p.num_groups > 1) close = keep_groups<VPL, float>(p, lane, u, tol);
+      id = take_best<VPL, float>(p, lane, u, tol, &close);
     }
-    id = take_best<VPL, float>(p, lane, u, tol, &close);
     if (close) id = select_in_double<VPL, LT>(p, row, lane);
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) u[i] = x[i] > -INFINITY ? order_of(x[i]) : 0u;
     bool close = false;
-    if (p.num_groups > 1) keep_groups<VPL, float>(p, lane, u, Exact());
-    id = take_best<VPL, float>(p, lane, u, Exact(), &close);
+    if (VPL <= 8 && sizeof(LT) == 2 && p.num_groups == 1) {
+      // a 16-bit logit's key has 13 zero bits at least below it (all ones, for the
+      // negative ones, whose low bits are cleared): room for the place
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (u[i] != 0) u[i] = (u[i] & ~1023u) | (uint32_t)(1023 - (lane * VPL + i));
+      sort_keys<VPL>(u);
+      id = take_sorted<VPL, true>(p, lane, u, Exact(), &close);
+    } else {
+      if (p.num_groups > 1) keep_groups<VPL, float>(p, lane, u, Exact());
+      id = take_best<VPL, float>(p, lane, u, Exact(), &close);
+    }
   }
   if (p.score == LORA_SCORE_SOFTMAX && !p.renormalize) {
     float m = -INFINITY;
@@ -459,6 +600,182 @@ __global__ void __launch_bounds__(kGrThreads, 1) group_kernel(const GroupParams 
   }
 }
 
+// Many pairs: three launches over all SMs, without a workspace.  pair_row is
+// written in full by the last one, so until then run b of the pairs holds its own
+// table (pairs per expert, then the rows before it) at its place in pair_row;
+// runs are at least E long.
+//   1. count: a CTA counts its run per expert;
+//   2. scan: one CTA turns the tables into rows before each run and the totals
+//      into expert_offsets;
+//   3. place: a CTA takes its table, ranks its run and writes the rows.
+
+constexpr int kRunThreads = 512;
+constexpr int kRunWarps = kRunThreads / 32;
+
+struct Runs {
+  int count, length;   // the last run takes the rest
+};
+
+LORA_DEV void run_bounds(const GroupParams& p, const Runs& r, int b, int* begin, int* end) {
+  *begin = b * r.length;
+  *end = b + 1 == r.count ? p.n : (b + 1) * r.length;
+}
+
+// Warp w's share of a run, and its table of pairs per expert.
+LORA_DEV void count_share(const GroupParams& p, int begin, int end, int* mine, bool* bad) {
+  const int lane = threadIdx.x & 31;
+  for (int e = lane; e < p.E; e += 32) mine[e] = 0;
+  __syncwarp();
+  for (int i0 = begin; i0 < end; i0 += 128) {
+    int e[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) e[q] = pair_expert(p, i0 + 32 * q + lane, end, bad);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t same = __match_any_sync(0xffffffffu, e[q]);
+      if (e[q] >= 0 && lane == __ffs((int)same) - 1) mine[e[q]] += __popc(same);
+      __syncwarp();
+    }
+  }
+}
+
+LORA_DEV void share_of(int begin, int end, int* lo, int* hi) {
+  const int warp = threadIdx.x >> 5;
+  const int per = ((end - begin + kRunWarps - 1) / kRunWarps + 31) / 32 * 32;
+  *lo = min(begin + warp * per, end);
+  *hi = min(*lo + per, end);
+}
+
+__global__ void __launch_bounds__(kRunThreads) group_count_kernel(const GroupParams p, const Runs r) {
+  extern __shared__ int gr_smem[];   // [E]
+  grid_dep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  int begin, end;
+  run_bounds(p, r, (int)blockIdx.x, &begin, &end);
+  for (int e = threadIdx.x; e < p.E; e += kRunThreads) gr_smem[e] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int i = begin + (int)threadIdx.x; i < end; i += kRunThreads) {
+    const int e = pair_expert(p, i, end, &bad);
+    if (e >= 0) atomicAdd(gr_smem + e, 1);
+  }
+  if (p.flags != nullptr && __any_sync(0xffffffffu, bad) && lane == 0)
+    raise_flag(p.flags, LORA_FLAG_BAD_EXPERT);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kRunThreads) p.pair_row[begin + e] = gr_smem[e];
+}
+
+constexpr int kScanThreads = 1024;
+
+__global__ void __launch_bounds__(kScanThreads) group_scan_kernel(const GroupParams p, const Runs r) {
+  __shared__ int scratch[kScanThreads / 32];
+  __shared__ int part[kScanThreads];
+  grid_dep_launch_dependents();
+  grid_dep_wait();
+  // `parts` threads per expert, each over a share of the runs
+  const int parts = kScanThreads / p.E > 0 ? kScanThreads / p.E : 1;   // E <= kScanThreads
+  const int per = (r.count + parts - 1) / parts;
+  const int e = threadIdx.x % p.E, q = threadIdx.x / p.E;
+  const int b0 = min(q * per, r.count), b1 = q < parts ? min(b0 + per, r.count) : b0;
+  int sum = 0;
+  for (int b = b0; b < b1; b += 8) {
+    int t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = b + k < b1 ? p.pair_row[(b + k) * r.length + e] : 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += t[k];
+  }
+  part[threadIdx.x] = q < parts ? sum : 0;
+  __syncthreads();
+  // totals per expert, their prefix, and the rows before this thread's share
+  int total = 0, before = 0;
+  if (threadIdx.x < p.E)
+    for (int k = 0; k < parts; ++k) total += part[k * p.E + threadIdx.x];
+  int rows = 0;
+  const int incl = block_inclusive_scan<kScanThreads>(total, scratch, &rows);
+  if (q < parts)
+    for (int k = 0; k < q; ++k) before += part[k * p.E + e];
+  __syncthreads();
+  if (threadIdx.x < p.E) {
+    part[threadIdx.x] = incl - total;   // first row of each expert
+    p.expert_offsets[threadIdx.x] = incl - total;
+  }
+  if (threadIdx.x == 0) p.expert_offsets[p.E] = rows;
+  __syncthreads();
+  int run = part[e] + before;
+  for (int b = b0; b < b1; b += 8) {
+    int t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = b + k < b1 ? p.pair_row[(b + k) * r.length + e] : 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (b + k < b1) p.pair_row[(b + k) * r.length + e] = run;
+      run += t[k];
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kRunThreads) group_place_kernel(const GroupParams p, const Runs r) {
+  extern __shared__ int gr_smem[];   // [kRunWarps][E]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int begin, end, lo, hi;
+  run_bounds(p, r, (int)blockIdx.x, &begin, &end);
+  share_of(begin, end, &lo, &hi);
+  int* mine = gr_smem + warp * p.E;
+  bool bad = false;
+  count_share(p, lo, hi, mine, &bad);
+  grid_dep_wait();   // the tables are there (the pairs are inputs of the whole call)
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += kRunThreads) {
+    int run = p.pair_row[begin + e];
+    for (int w = 0; w < kRunWarps; ++w) {
+      const int c = gr_smem[w * p.E + e];
+      gr_smem[w * p.E + e] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  for (int i0 = lo; i0 < hi; i0 += 128) {
+    int ex[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) ex[q] = pair_expert(p, i0 + 32 * q + lane, hi, &bad);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + 32 * q + lane;
+      const uint32_t same = __match_any_sync(0xffffffffu, ex[q]);
+      int row = -1;
+      if (ex[q] >= 0) row = mine[ex[q]] + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (ex[q] >= 0 && lane == __ffs((int)same) - 1) mine[ex[q]] += __popc(same);
+      __syncwarp();
+      if (i < hi) {
+        p.pair_row[i] = row;
+        if (row >= 0) {
+          const int t = i / p.top_k;
+          p.row_token[row] = t;
+          if (p.row_slot != nullptr) p.row_slot[row] = __ldg(p.token_slot + t);
+        }
+      }
+    }
+  }
+}
+
+template <typename K>
+cudaError_t launch_after(K kernel, int grid, int threads, size_t smem, bool overlap,
+                         cudaStream_t stream, const GroupParams& p, const Runs& r) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3((unsigned)threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p, r);
+}
+
 // ---------------------------------------------------------------------------
 // Combine: out[t] = residual[t] + sum_j w[t, j] y[pair_row[t, j]], fp32, in
 // order of j, rounded once.  A thread owns eight columns of one token.
@@ -546,8 +863,23 @@ cudaError_t group_launch(const GroupParams& p, cudaStream_t stream) {
       err = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (kGrWarps + 1) * kRouteMaxExperts * 4);
       if (err != cudaSuccess) return err;
+      err = cudaFuncSetAttribute(group_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kRunWarps * kRouteMaxExperts * 4);
+      if (err != cudaSuccess) return err;
       g_group_attr[dev] = true;
     }
+  }
+  if (p.n > 16384) {
+    Runs r;
+    r.length = p.E > 1024 ? p.E : 1024;
+    while (p.n / r.length > 592) r.length *= 2;
+    r.count = p.n / r.length;
+    err = launch_after(group_count_kernel, r.count, kRunThreads, (size_t)p.E * 4, false, stream, p, r);
+    if (err != cudaSuccess) return err;
+    err = launch_after(group_scan_kernel, 1, kScanThreads, 0, true, stream, p, r);
+    if (err != cudaSuccess) return err;
+    return launch_after(group_place_kernel, r.count, kRunThreads, (size_t)kRunWarps * p.E * 4, true,
+                        stream, p, r);
   }
   // one CTA per 4096 pairs, up to a cluster of eight
   int ctas = 1;
