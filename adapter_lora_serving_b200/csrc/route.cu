@@ -146,7 +146,7 @@ LORA_DEV uint32_t magnitude_of(double) { return 0; }   // (kExact only)
 //     sum by 2.5 u and half a u for each of VPL + 5 additions, the quotient and the
 //     product by 2.5 u more: (8 + (VPL + 5) / 2) u smax.
 //   the bias sum: half a u of the key; the place within the lane that fills its
-//     lowest bits (SortedKeys): 8 u at most of it.
+//     lowest bits (Sorted): 8 u at most of it.
 // A pair's sum has the errors of both its keys, whose magnitudes its own can be
 // far below: `of_sum` has the row's largest.
 struct Within {
@@ -276,108 +276,161 @@ LORA_DEV void make_keys(const RouteParams& p, int lane, const float (&x)[VPL],
   }
 }
 
-// A lane's keys (VPL <= 8) in descending order, for the fp32 selection whose close
-// calls are decided elsewhere, or on 16-bit logits: the lowest bits of a key hold
-// the expert's place (LB bits: 7 - i within the lane for approximate keys, 1023 - e
-// for 16-bit ones, which are exact and never tie then).  One sorting network, after
-// which a round of the selection looks at the lanes' first keys alone.
+// Batcher's odd-even merge sort of the VPL keys of a lane, descending.
+template <int VPL, typename Swap>
+LORA_DEV void sort_network(Swap order) {
+#pragma unroll
+  for (int p = 1; p < VPL; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < VPL; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < VPL && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order(i + j, i + j + k);
+}
+
+// A lane's keys (VPL <= 8; with 16 the rounds over unsorted keys are faster, 29 us
+// against 39 for 8192 x 384) in descending order: one sorting network, after which a
+// round of the selection looks at the lanes' first keys alone (the list of the lane
+// that gave one moves up).  Equal keys stay in order of their places.
+// Where the place in the lane is held:
+//   kLow    in the key's four lowest bits (15 - i), which changes an approximate
+//           key by 15 ulps at most (accounted for in Within);
+//   kExpert in the ten lowest bits (1023 - e) of a 16-bit logit's key, whose own
+//           lowest 13 are constant: exact, and no two are equal;
+//   kBeside beside the key: exact keys that need all their bits.
+enum Place { kLow, kExpert, kBeside };
+
+template <int VPL, typename V, Place kPlace>
+struct Sorted {
+  typedef typename KeyOf<V>::U U;
+  U u[VPL];
+  int at[kPlace == kBeside ? VPL : 1];
+
+  LORA_DEV void sort(int lane) {
+    if (kPlace == kBeside) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) at[kPlace == kBeside ? i : 0] = i;
+      sort_network<VPL>([&](int i, int j) {
+        const int ai = at[kPlace == kBeside ? i : 0], aj = at[kPlace == kBeside ? j : 0];
+        const bool swap = u[j] > u[i] || (u[j] == u[i] && aj < ai);
+        const U hi = swap ? u[j] : u[i];
+        u[j] = swap ? u[i] : u[j];
+        u[i] = hi;
+        at[kPlace == kBeside ? i : 0] = swap ? aj : ai;
+        at[kPlace == kBeside ? j : 0] = swap ? ai : aj;
+      });
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (u[i] != 0)
+          u[i] = kPlace == kLow ? (u[i] & ~(U)15) | (U)(15 - i)
+                                : (u[i] & ~(U)1023) | (U)(1023 - (lane * VPL + i));
+      sort_network<VPL>([&](int i, int j) {
+        const U hi = max(u[i], u[j]);
+        u[j] = min(u[i], u[j]);
+        u[i] = hi;
+      });
+    }
+  }
+
+  // keep_groups for groups of `span` whole lanes, a power of two of them.
+  template <typename Tol>
+  LORA_DEV bool keep(const RouteParams& p, int lane, int span, Tol tol) {
+    U a = u[0], b = VPL > 1 ? u[VPL > 1 ? 1 : 0] : (U)0;
+    for (int o = 1; o < span; o <<= 1) {
+      const U c = __shfl_xor_sync(0xffffffffu, a, o), d = __shfl_xor_sync(0xffffffffu, b, o);
+      b = max(min(a, c), max(b, d));
+      a = max(a, c);
+    }
+    // every lane of a group has its score; equal scores rank by group
+    U score = a;
+    if (p.group_score == LORA_GROUP_TOP_PAIR && b != 0) score = order_of(value_of(a) + value_of(b));
+    const int mine = lane / span;
+    int rank = 0;
+    for (int g = 0; g < p.num_groups; ++g) {
+      const U other = __shfl_sync(0xffffffffu, score, g * span);
+      rank += (other > score || (other == score && g < mine)) ? 1 : 0;
+    }
+    const bool real = mine < p.num_groups;
+    const bool kept = real && rank < p.top_groups;
+    bool close = false;
+    if (!Tol::kExact) {
+      const U worst_kept = ~warp_max(kept && score != 0 ? (U)~score : (U)0);
+      const U best_out = warp_max(real && !kept ? score : (U)0);
+      const uint32_t magnitude =
+          max(a != 0 ? magnitude_of(value_of(a)) : 0u, b != 0 ? magnitude_of(value_of(b)) : 0u);
+      const float border = tol.of_sum(magnitude);
+      close = best_out != 0 && value_of(worst_kept) - value_of(best_out) <= border;
+    }
+    if (!kept) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) u[i] = 0;
+    }
+    return close;
+  }
+
+  // take_best
+  template <typename Tol>
+  LORA_DEV int take(const RouteParams& p, int lane, Tol tol, bool* close) {
+    int id = -1;
+    U prev = 0;
+    const int rounds = p.top_k + (Tol::kExact ? 0 : 1);
+    for (int j = 0; j < rounds; ++j) {
+      const U m = warp_max(u[0]);
+      if (m == 0) break;
+      if (!Tol::kExact) {
+        if (prev != 0 && value_of(prev) - value_of(m) <= tol(value_of(prev))) *close = true;
+        prev = m;
+        if (j == p.top_k) break;
+      }
+      const int src = __ffs((int)__ballot_sync(0xffffffffu, u[0] == m)) - 1;
+      int e;
+      if (kPlace == kBeside) e = src * VPL + __shfl_sync(0xffffffffu, at[0], src);
+      else if (kPlace == kLow) e = src * VPL + 15 - (int)(m & 15u);
+      else e = 1023 - (int)(m & 1023u);
+      if (lane == j) id = e;
+      if (lane == src) {
+#pragma unroll
+        for (int i = 0; i + 1 < VPL; ++i) {
+          u[i] = u[i + 1];
+          if (kPlace == kBeside) at[kPlace == kBeside ? i : 0] = at[kPlace == kBeside ? i + 1 : 0];
+        }
+        u[VPL - 1] = 0;
+      }
+    }
+    return id;
+  }
+};
+
+// Lanes per expert group where groups are whole lanes, a power of two of them;
+// else 0.
 template <int VPL>
-LORA_DEV void sort_keys(uint32_t (&u)[VPL]) {
-  auto order = [&](int i, int j) {
-    const uint32_t hi = max(u[i], u[j]);
-    u[j] = min(u[i], u[j]);
-    u[i] = hi;
-  };
-  if (VPL == 2) {
-    order(0, 1);
-  } else if (VPL == 4) {
-    order(0, 2); order(1, 3); order(0, 1); order(2, 3); order(1, 2);
-  } else if (VPL == 8) {
-    // Batcher's odd-even merge sort, 19 comparators
-    order(0, 1); order(2, 3); order(4, 5); order(6, 7);
-    order(0, 2); order(1, 3); order(4, 6); order(5, 7);
-    order(1, 2); order(5, 6);
-    order(0, 4); order(1, 5); order(2, 6); order(3, 7);
-    order(2, 4); order(3, 5);
-    order(1, 2); order(3, 4); order(5, 6);
-  }
+LORA_DEV int group_span(const RouteParams& p) {
+  const int n = p.E / p.num_groups;
+  const int span = n / VPL;
+  return n % VPL == 0 && (span & (span - 1)) == 0 ? span : 0;
 }
 
-// take_best on sorted keys.  kPlace: the keys carry the expert (1023 - e) and are
-// exact; else they carry 7 - i.
-template <int VPL, bool kPlace, typename Tol>
-LORA_DEV int take_sorted(const RouteParams& p, int lane, uint32_t (&u)[VPL], Tol tol, bool* close) {
-  int id = -1;
-  uint32_t prev = 0;
-  const int rounds = p.top_k + (kPlace ? 0 : 1);
-  for (int j = 0; j < rounds; ++j) {
-    const uint32_t m = warp_max(u[0]);
-    if (m == 0) break;
-    if (!kPlace) {
-      if (prev != 0 && value_of(prev) - value_of(m) <= tol(value_of(prev))) *close = true;
-      prev = m;
-      if (j == p.top_k) break;
-    }
-    const uint32_t holders = __ballot_sync(0xffffffffu, u[0] == m);
-    const int src = __ffs((int)holders) - 1;
-    if (lane == j) id = kPlace ? 1023 - (int)(m & 1023u) : src * VPL + 7 - (int)(m & 7u);
-    if (lane == src) {
-#pragma unroll
-      for (int i = 0; i + 1 < VPL; ++i) u[i] = u[i + 1];
-      u[VPL - 1] = 0;
-    }
-  }
-  return id;
-}
-
-// keep_groups on sorted keys, for groups of `span` whole lanes (a power of two).
-template <int VPL, typename Tol>
-LORA_DEV bool keep_sorted_groups(const RouteParams& p, int lane, int span, uint32_t (&u)[VPL],
-                                 Tol tol) {
-  const bool pair = p.group_score == LORA_GROUP_TOP_PAIR;
-  uint32_t a = u[0], b = VPL > 1 ? u[VPL > 1 ? 1 : 0] : 0u;
-  for (int o = 1; o < span; o <<= 1) {
-    const uint32_t c = __shfl_xor_sync(0xffffffffu, a, o), d = __shfl_xor_sync(0xffffffffu, b, o);
-    b = max(min(a, c), max(b, d));
-    a = max(a, c);
-  }
-  // every lane of a group has its score; equal scores rank by group
-  uint32_t score = a;
-  if (pair && b != 0) score = order_of(value_of(a) + value_of(b));
-  int rank = 0;
-  const int mine = lane / span;
-  for (int g = 0; g < p.num_groups; ++g) {
-    const uint32_t other = __shfl_sync(0xffffffffu, score, g * span);
-    rank += (other > score || (other == score && g < mine)) ? 1 : 0;
-  }
-  const bool real = mine < p.num_groups;
-  const bool kept = real && rank < p.top_groups;
-  bool close = false;
-  if (!Tol::kExact) {
-    const uint32_t worst_kept = ~warp_max(kept && score != 0 ? ~score : 0u);
-    const uint32_t best_out = warp_max(real && !kept ? score : 0u);
-    const uint32_t magnitude =
-        max(a != 0 ? magnitude_of(value_of(a)) : 0u, b != 0 ? magnitude_of(value_of(b)) : 0u);
-    const float border = tol.of_sum(magnitude);
-    close = best_out != 0 && value_of(worst_kept) - value_of(best_out) <= border;
-  }
-  if (!kept) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) u[i] = 0;
-  }
-  return close;
-}
-
-// The same selection in 64 bits, for the tokens whose fp32 keys come too close
-// to tell apart.
+// The same selection in 64 bits, for the tokens whose fp32 keys come too close to
+// tell apart.
 template <int VPL, typename LT>
 __device__ __noinline__ int select_in_double(const RouteParams& p, const LT* row, int lane) {
   float x[VPL];
   double s[VPL];
-  uint64_t u[VPL];
   bool bad = false, close = false;
   load_row<VPL, LT>(row, lane, p.E, x, &bad);
   scores<VPL, double>(p, lane, x, s);
+  const int span = p.num_groups > 1 ? group_span<VPL>(p) : 1;
+  if (VPL <= 8 && span > 0) {
+    Sorted<VPL, double, kBeside> k;
+    make_keys<VPL, double>(p, lane, x, s, k.u, &bad);
+    k.sort(lane);
+    if (p.num_groups > 1) k.keep(p, lane, span, Exact());
+    return k.take(p, lane, Exact(), &close);
+  }
+  uint64_t u[VPL];
   make_keys<VPL, double>(p, lane, x, s, u, &bad);
   if (p.num_groups > 1) keep_groups<VPL, double>(p, lane, u, Exact());
   return take_best<VPL, double>(p, lane, u, Exact(), &close);
@@ -396,50 +449,43 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
   if (t >= p.T) return;
   const LT* row = reinterpret_cast<const LT*>(p.logits) + (size_t)t * p.E;
   float x[VPL];
-  uint32_t u[VPL];
-  bool bad = false;
+  bool bad = false, close = false;
   load_row<VPL, LT>(row, lane, p.E, x, &bad);
   const bool pair = p.num_groups > 1 && p.group_score == LORA_GROUP_TOP_PAIR;
   const bool by_score = p.bias != nullptr || pair;
+  const int span = p.num_groups > 1 ? group_span<VPL>(p) : 1;
   int id;
   float inv_sum = 1.0f, row_max = 0.0f;   // softmax normalisation, where it is needed
-  // groups of whole lanes, a power of two of them
-  const int span = p.num_groups > 1 && p.E / p.num_groups % VPL == 0 ? p.E / p.num_groups / VPL : 0;
-  const bool lanes_fit = p.num_groups == 1 || (span > 0 && (span & (span - 1)) == 0);
   if (by_score) {
     float s[VPL];
     const float smax = scores<VPL, float>(p, lane, x, s);
-    make_keys<VPL, float>(p, lane, x, s, u, &bad);
     const Within tol = key_error<VPL>(smax);
-    bool close = false;
-    if (VPL <= 8 && lanes_fit) {
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (u[i] != 0) u[i] = (u[i] & ~7u) | (uint32_t)(7 - i);
-      sort_keys<VPL>(u);
-      if (p.num_groups > 1) close = keep_sorted_groups<VPL>(p, lane, span, u, tol);
-      id = take_sorted<VPL, false>(p, lane, u, tol, &close);
+    if (VPL <= 8 && span > 0) {
+      Sorted<VPL, float, kLow> k;
+      make_keys<VPL, float>(p, lane, x, s, k.u, &bad);
+      k.sort(lane);
+      if (p.num_groups > 1) close = k.keep(p, lane, span, tol);
+      id = k.take(p, lane, tol, &close);
     } else {
+      uint32_t u[VPL];
+      make_keys<VPL, float>(p, lane, x, s, u, &bad);
       if (p.num_groups > 1) close = keep_groups<VPL, float>(p, lane, u, tol);
       id = take_best<VPL, float>(p, lane, u, tol, &close);
     }
     if (close) id = select_in_double<VPL, LT>(p, row, lane);
+  } else if (VPL <= 8 && span > 0) {
+    Sorted<VPL, float, sizeof(LT) == 2 ? kExpert : kBeside> k;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) k.u[i] = x[i] > -INFINITY ? order_of(x[i]) : 0u;
+    k.sort(lane);
+    if (p.num_groups > 1) k.keep(p, lane, span, Exact());
+    id = k.take(p, lane, Exact(), &close);
   } else {
+    uint32_t u[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) u[i] = x[i] > -INFINITY ? order_of(x[i]) : 0u;
-    bool close = false;
-    if (VPL <= 8 && sizeof(LT) == 2 && p.num_groups == 1) {
-      // a 16-bit logit's key has 13 zero bits at least below it (all ones, for the
-      // negative ones, whose low bits are cleared): room for the place
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (u[i] != 0) u[i] = (u[i] & ~1023u) | (uint32_t)(1023 - (lane * VPL + i));
-      sort_keys<VPL>(u);
-      id = take_sorted<VPL, true>(p, lane, u, Exact(), &close);
-    } else {
-      if (p.num_groups > 1) keep_groups<VPL, float>(p, lane, u, Exact());
-      id = take_best<VPL, float>(p, lane, u, Exact(), &close);
-    }
+    if (p.num_groups > 1) keep_groups<VPL, float>(p, lane, u, Exact());
+    id = take_best<VPL, float>(p, lane, u, Exact(), &close);
   }
   if (p.score == LORA_SCORE_SOFTMAX && !p.renormalize) {
     float m = -INFINITY;
