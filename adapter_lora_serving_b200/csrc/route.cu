@@ -16,13 +16,13 @@ namespace lora {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Ordered keys: unsigned integers that compare as the finite numbers they come
-// from (+0 and -0 alike); 0 is below all of them and marks what cannot be chosen.
+// Ordered keys: unsigned integers that compare as the numbers they come from
+// (+0 and -0 alike).  What cannot be chosen has the key of -inf, or 0.
 // ---------------------------------------------------------------------------
 
 LORA_DEV uint32_t order_of(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
 }
 LORA_DEV float value_of(uint32_t u) {
   return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
@@ -34,6 +34,8 @@ LORA_DEV uint64_t order_of(double v) {
 LORA_DEV double value_of(uint64_t u) {
   return __longlong_as_double((long long)((u >> 63) ? (u & 0x7fffffffffffffffull) : ~u));
 }
+LORA_DEV bool is_open(uint32_t u) { return u > 0x007fffffu; }
+LORA_DEV bool is_open(uint64_t u) { return u > 0x000fffffffffffffull; }
 
 LORA_DEV uint32_t warp_max(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 LORA_DEV uint64_t warp_max(uint64_t v) {
@@ -50,11 +52,10 @@ struct KeyOf<float> { typedef uint32_t U; };
 template <>
 struct KeyOf<double> { typedef uint64_t U; };
 
-// The warp's row of logits: lane l holds experts [l * VPL, (l + 1) * VPL).
-// Experts past E, and those whose logit is -inf, NaN or +inf, come as -inf;
-// the last two set *bad.
+// The warp's row of logits: lane l holds experts [l * VPL, (l + 1) * VPL), those
+// past E as -inf.
 template <int VPL, typename LT>
-LORA_DEV void load_row(const LT* row, int lane, int E, float (&x)[VPL], bool* bad) {
+LORA_DEV void load_row(const LT* row, int lane, int E, float (&x)[VPL]) {
   const int e0 = lane * VPL;
   constexpr int kBytes = VPL * (int)sizeof(LT);
   if (E % VPL == 0 && kBytes >= 4) {
@@ -87,36 +88,61 @@ LORA_DEV void load_row(const LT* row, int lane, int E, float (&x)[VPL], bool* ba
 #pragma unroll
     for (int i = 0; i < VPL; ++i) x[i] = e0 + i < E ? to_f32(row[e0 + i]) : -INFINITY;
   }
+}
+
+// Masked logits: NaN and +inf become -inf (and set *bad).  Returns whether every
+// lane's share is finite, or wholly past E.
+template <int VPL>
+LORA_DEV bool mask_row(float (&x)[VPL], bool past_end, bool* bad) {
+  bool fine = true;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) fine = fine && fabsf(x[i]) < INFINITY;
+  if (__all_sync(0xffffffffu, fine || past_end)) return true;
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
-    if (!(x[i] < INFINITY)) {   // NaN or +inf
+    if (!(x[i] < INFINITY)) {
       x[i] = -INFINITY;
       *bad = true;
     }
+  return false;
 }
 
-// e^z and a / b: in 64 bits, or for fp32 keys whose error is accounted for (Within)
+// The lane's biases: 0 without any, -inf past E and where one is NaN or +inf
+// (*bad).
+template <int VPL>
+LORA_DEV void load_bias(const RouteParams& p, int lane, float (&bias)[VPL], bool* bad) {
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = lane * VPL + i;
+    bias[i] = e >= p.E ? -INFINITY : p.bias != nullptr ? __ldg(p.bias + e) : 0.0f;
+    if (!(bias[i] < INFINITY)) {
+      bias[i] = -INFINITY;
+      *bad = true;
+    }
+  }
+}
+
+// e^z and 1 / a: in 64 bits, or for fp32 keys whose error is accounted for (Within)
 // the fast ones: 2 + 1.173 |z| ulps and 2 ulps.
 LORA_DEV double power(double z) { return exp(z); }
 LORA_DEV float power(float z) { return __expf(z); }
-LORA_DEV double quotient(double a, double b) { return a / b; }
-LORA_DEV float quotient(float a, float b) { return __fdividef(a, b); }
+LORA_DEV double inverse(double a) { return 1.0 / a; }
+LORA_DEV float inverse(float a) { return __fdividef(1.0f, a); }
 
-// Scores s of the lane's experts and their selection keys s + bias, in V.
-// Returns the largest score of the row.
+// Scores of the lane's experts in V.  Returns the largest score of the row.
 template <int VPL, typename V>
-LORA_DEV V scores(const RouteParams& p, int lane, const float (&x)[VPL], V (&s)[VPL]) {
+LORA_DEV V scores(const RouteParams& p, const float (&x)[VPL], V (&s)[VPL]) {
   if (p.score == LORA_SCORE_SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) s[i] = quotient((V)1, (V)1 + power(-(V)x[i]));
+    for (int i = 0; i < VPL; ++i) s[i] = inverse((V)1 + power(-(V)x[i]));
     return (V)1;
   }
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
   {
-    const uint32_t u = warp_max(m > -INFINITY ? order_of(m) : 0u);
-    m = u != 0u ? value_of(u) : 0.0f;
+    const uint32_t u = warp_max(order_of(m));
+    m = is_open(u) ? value_of(u) : 0.0f;
   }
   V sum = 0;
 #pragma unroll
@@ -126,19 +152,38 @@ LORA_DEV V scores(const RouteParams& p, int lane, const float (&x)[VPL], V (&s)[
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const V inv = (V)1 / sum;
+  const V inv = inverse(sum);
 #pragma unroll
   for (int i = 0; i < VPL; ++i) s[i] = s[i] * inv;
   return inv;   // the largest: exp(0) / sum
 }
 
+// Selection keys s + bias of the lane's experts; a masked logit has key 0, a masked
+// bias the key of -inf.
+template <int VPL, typename V>
+LORA_DEV void make_keys(const float (&x)[VPL], const V (&s)[VPL], const float (&bias)[VPL],
+                        bool finite, typename KeyOf<V>::U (&u)[VPL]) {
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) u[i] = order_of(s[i] + (V)bias[i]);
+  if (!finite) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (!(x[i] > -INFINITY)) u[i] = 0;
+  }
+}
+
+LORA_DEV uint32_t magnitude_of(uint32_t u) {
+  return is_open(u) ? __float_as_uint(fabsf(value_of(u))) : 0u;
+}
+LORA_DEV uint32_t magnitude_of(uint64_t) { return 0; }   // (exact keys only)
+
+// How close two keys may come before fp32 cannot tell them apart.
 struct Exact {
   static constexpr bool kExact = true;
   template <typename V>
   LORA_DEV V operator()(V) const { return (V)-1; }
   LORA_DEV float of_sum(uint32_t) const { return -1.0f; }
 };
-LORA_DEV uint32_t magnitude_of(double) { return 0; }   // (kExact only)
 // Twice the error of an fp32 key, in units of u = 2^-23.
 //   sigmoid: e^-x moves the score by s (1 - s) (2 + 1.173 |x|) u < u (|x| s (1 - s)
 //     < .23); the sum and the quotient by 3 s u: 4 u of the largest score, 1.
@@ -157,25 +202,49 @@ struct Within {
     return 2.0f * of_score + 0x1p-17f * __uint_as_float(warp_max(magnitude));
   }
 };
-LORA_DEV uint32_t magnitude_of(float v) { return __float_as_uint(fabsf(v)); }
 template <int VPL>
 LORA_DEV Within key_error(float smax) {
   Within w = {(float)(16 + VPL + 6) * 0x1p-23f * smax};
   return w;
 }
 
+// Ranks the groups' scores, lane g holding group g's (`count` of them): which
+// groups are kept, as a mask, and whether the border is within the error.
+template <typename U, typename Tol>
+LORA_DEV uint32_t best_groups(const RouteParams& p, int lane, U score, uint32_t magnitude, Tol tol,
+                              bool* close) {
+  const bool real = lane < p.num_groups;
+  int rank = 0;
+  for (int g = 0; g < p.num_groups; ++g) {
+    const U other = __shfl_sync(0xffffffffu, score, g);
+    rank += (other > score || (other == score && g < lane)) ? 1 : 0;
+  }
+  const bool kept = real && rank < p.top_groups;
+  const uint32_t keep = __ballot_sync(0xffffffffu, kept && is_open(score));
+  if (!Tol::kExact) {
+    const U worst_kept = ~warp_max(kept && is_open(score) ? (U)~score : (U)0);
+    const U best_out = warp_max(real && !kept ? score : (U)0);
+    const float border = tol.of_sum(magnitude);
+    *close |= is_open(best_out) && value_of(worst_kept) - value_of(best_out) <= border;
+  }
+  return keep;
+}
+
+// A pair's score from the two largest keys of a group (one alone counts alone).
+template <typename U>
+LORA_DEV U group_score_of(const RouteParams& p, U top, U second) {
+  return p.group_score == LORA_GROUP_TOP_PAIR && is_open(second)
+             ? order_of(value_of(top) + value_of(second))
+             : top;
+}
+
 // Keeps the experts of the best top_groups groups (ties to the lowest group),
-// clearing the others' keys.  Group g holds the n = E / num_groups experts from
-// g * n on; its score is its largest key, or the sum of its two largest (one
-// alone counts alone).  Lane g holds group g's score while they are compared.
-// Returns whether the border between kept and dropped is within tol(value).
-template <int VPL, typename V, typename Tol>
-LORA_DEV bool keep_groups(const RouteParams& p, int lane, typename KeyOf<V>::U (&u)[VPL],
-                          Tol tol) {
-  typedef typename KeyOf<V>::U U;
+// clearing the others' keys.  Group g holds the E / num_groups experts from
+// g * E / num_groups on.  Any group size.
+template <int VPL, typename U, typename Tol>
+LORA_DEV void keep_groups(const RouteParams& p, int lane, U (&u)[VPL], Tol tol, bool* close) {
   const int n = p.E / p.num_groups;
-  const bool pair = p.group_score == LORA_GROUP_TOP_PAIR;
-  U mine = 0;   // this lane's group's score
+  U score = 0;   // this lane's group's
   uint32_t magnitude = 0;
   for (int g = 0; g < p.num_groups; ++g) {
     U a = 0, b = 0;   // the lane's two largest keys in group g
@@ -187,48 +256,30 @@ LORA_DEV bool keep_groups(const RouteParams& p, int lane, typename KeyOf<V>::U (
       a = max(a, v);
     }
     const U top = warp_max(a);
-    U score = top;
-    if (pair && top != 0) {
-      // the second largest: the best lane's runner-up, or another lane's best
+    U second = 0;
+    if (p.group_score == LORA_GROUP_TOP_PAIR) {
+      // the best lane's runner-up, or another lane's best
       const uint32_t holders = __ballot_sync(0xffffffffu, a == top);
-      const bool first = lane == __ffs((int)holders) - 1;
-      const U second = warp_max(first ? b : a);
-      if (second != 0) score = order_of(value_of(top) + value_of(second));
+      second = warp_max(lane == __ffs((int)holders) - 1 ? b : a);
     }
-    if (lane == g) mine = score;
-    if (!Tol::kExact && a != 0) magnitude = max(magnitude, max(magnitude_of(value_of(a)), b != 0 ? magnitude_of(value_of(b)) : 0u));
+    const U of_group = group_score_of(p, top, second);
+    if (lane == g) score = of_group;
+    if (!Tol::kExact) magnitude = max(magnitude, max(magnitude_of(a), magnitude_of(b)));
   }
-  // rank of this lane's group among all
-  int rank = 0;
-  for (int g = 0; g < p.num_groups; ++g) {
-    const U other = __shfl_sync(0xffffffffu, mine, g);
-    rank += (other > mine || (other == mine && g < lane)) ? 1 : 0;
-  }
-  const bool kept = lane < p.num_groups && rank < p.top_groups && mine != 0;
-  const uint32_t keep = __ballot_sync(0xffffffffu, kept);
-  const U worst_kept = ~warp_max(kept ? (U)~mine : (U)0);   // smallest kept score
-  const U best_out = warp_max(lane < p.num_groups && !kept ? mine : (U)0);
-  bool close = false;
-  if (!Tol::kExact) {
-    const float border = tol.of_sum(magnitude);
-    close = best_out != 0 && keep != 0 && value_of(worst_kept) - value_of(best_out) <= border;
-  }
+  const uint32_t keep = best_groups(p, lane, score, magnitude, tol, close);
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     const int e = lane * VPL + i;
     if (e < p.E && !((keep >> (e / n)) & 1u)) u[i] = 0;
   }
-  return close;
 }
 
 // The top_k largest keys in descending order, ties to the lowest expert: lane
 // j returns the j-th choice (-1 when nothing is left).  *close is set when two
 // neighbours in that order, or the last choice and the best one left, are
-// within tol(value) of each other (Tol::kExact: not looked at).
-template <int VPL, typename V, typename Tol>
-LORA_DEV int take_best(const RouteParams& p, int lane, typename KeyOf<V>::U (&u)[VPL], Tol tol,
-                       bool* close) {
-  typedef typename KeyOf<V>::U U;
+// within the keys' error.
+template <int VPL, typename U, typename Tol>
+LORA_DEV int take_best(const RouteParams& p, int lane, U (&u)[VPL], Tol tol, bool* close) {
   U best = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) best = max(best, u[i]);
@@ -237,11 +288,12 @@ LORA_DEV int take_best(const RouteParams& p, int lane, typename KeyOf<V>::U (&u)
   const int rounds = p.top_k + (Tol::kExact ? 0 : 1);
   for (int j = 0; j < rounds; ++j) {
     const U m = warp_max(best);
-    if (m == 0) break;
-    if (!Tol::kExact && prev != 0 && value_of(prev) - value_of(m) <= tol(value_of(prev)))
-      *close = true;
-    prev = m;
-    if (j == p.top_k) break;
+    if (!is_open(m)) break;
+    if (!Tol::kExact) {
+      if (prev != 0 && value_of(prev) - value_of(m) <= tol(value_of(prev))) *close = true;
+      prev = m;
+      if (j == p.top_k) break;
+    }
     const int src = __ffs((int)__ballot_sync(0xffffffffu, best == m)) - 1;
     int at = 0;
     if (lane == src) {
@@ -261,21 +313,6 @@ LORA_DEV int take_best(const RouteParams& p, int lane, typename KeyOf<V>::U (&u)
   return id;
 }
 
-// Selection keys s + bias of the lane's experts; experts with a masked logit or
-// bias get key 0.
-template <int VPL, typename V>
-LORA_DEV void make_keys(const RouteParams& p, int lane, const float (&x)[VPL],
-                        const V (&s)[VPL], typename KeyOf<V>::U (&u)[VPL], bool* bad) {
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const int e = lane * VPL + i;
-    float b = 0.0f;
-    if (p.bias != nullptr && e < p.E) b = __ldg(p.bias + e);
-    if (!(b < INFINITY)) *bad = true;
-    u[i] = (x[i] > -INFINITY && b > -INFINITY && b < INFINITY) ? order_of(s[i] + (V)b) : 0;
-  }
-}
-
 // Batcher's odd-even merge sort of the VPL keys of a lane, descending.
 template <int VPL, typename Swap>
 LORA_DEV void sort_network(Swap order) {
@@ -291,10 +328,10 @@ LORA_DEV void sort_network(Swap order) {
 }
 
 // A lane's keys (VPL <= 8; with 16 the rounds over unsorted keys are faster, 29 us
-// against 39 for 8192 x 384) in descending order: one sorting network, after which a
-// round of the selection looks at the lanes' first keys alone (the list of the lane
-// that gave one moves up).  Equal keys stay in order of their places.
-// Where the place in the lane is held:
+// against 39 for 8192 tokens of 384 experts) in descending order: one sorting
+// network, after which a round of the selection looks at the lanes' first keys
+// alone (the list of the lane that gave one moves up).  Equal keys stay in order of
+// their places.  Where the place in the lane is held:
 //   kLow    in the key's four lowest bits (15 - i), which changes an approximate
 //           key by 15 ulps at most (accounted for in Within);
 //   kExpert in the ten lowest bits (1023 - e) of a 16-bit logit's key, whose own
@@ -305,28 +342,28 @@ enum Place { kLow, kExpert, kBeside };
 template <int VPL, typename V, Place kPlace>
 struct Sorted {
   typedef typename KeyOf<V>::U U;
+  static constexpr bool kAt = kPlace == kBeside;
   U u[VPL];
-  int at[kPlace == kBeside ? VPL : 1];
+  int at[kAt ? VPL : 1];
 
   LORA_DEV void sort(int lane) {
-    if (kPlace == kBeside) {
+    if (kAt) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) at[kPlace == kBeside ? i : 0] = i;
+      for (int i = 0; i < VPL; ++i) at[kAt ? i : 0] = i;
       sort_network<VPL>([&](int i, int j) {
-        const int ai = at[kPlace == kBeside ? i : 0], aj = at[kPlace == kBeside ? j : 0];
+        const int ai = at[kAt ? i : 0], aj = at[kAt ? j : 0];
         const bool swap = u[j] > u[i] || (u[j] == u[i] && aj < ai);
         const U hi = swap ? u[j] : u[i];
         u[j] = swap ? u[i] : u[j];
         u[i] = hi;
-        at[kPlace == kBeside ? i : 0] = swap ? aj : ai;
-        at[kPlace == kBeside ? j : 0] = swap ? ai : aj;
+        at[kAt ? i : 0] = swap ? aj : ai;
+        at[kAt ? j : 0] = swap ? ai : aj;
       });
     } else {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        if (u[i] != 0)
-          u[i] = kPlace == kLow ? (u[i] & ~(U)15) | (U)(15 - i)
-                                : (u[i] & ~(U)1023) | (U)(1023 - (lane * VPL + i));
+        u[i] = kPlace == kLow ? (u[i] & ~(U)15) | (U)(15 - i)
+                              : (u[i] & ~(U)1023) | (U)(1023 - (lane * VPL + i));
       sort_network<VPL>([&](int i, int j) {
         const U hi = max(u[i], u[j]);
         u[j] = min(u[i], u[j]);
@@ -337,70 +374,67 @@ struct Sorted {
 
   // keep_groups for groups of `span` whole lanes, a power of two of them.
   template <typename Tol>
-  LORA_DEV bool keep(const RouteParams& p, int lane, int span, Tol tol) {
+  LORA_DEV void keep(const RouteParams& p, int lane, int span, Tol tol, bool* close) {
     U a = u[0], b = VPL > 1 ? u[VPL > 1 ? 1 : 0] : (U)0;
     for (int o = 1; o < span; o <<= 1) {
       const U c = __shfl_xor_sync(0xffffffffu, a, o), d = __shfl_xor_sync(0xffffffffu, b, o);
       b = max(min(a, c), max(b, d));
       a = max(a, c);
     }
-    // every lane of a group has its score; equal scores rank by group
-    U score = a;
-    if (p.group_score == LORA_GROUP_TOP_PAIR && b != 0) score = order_of(value_of(a) + value_of(b));
-    const int mine = lane / span;
-    int rank = 0;
-    for (int g = 0; g < p.num_groups; ++g) {
-      const U other = __shfl_sync(0xffffffffu, score, g * span);
-      rank += (other > score || (other == score && g < mine)) ? 1 : 0;
-    }
-    const bool real = mine < p.num_groups;
-    const bool kept = real && rank < p.top_groups;
-    bool close = false;
-    if (!Tol::kExact) {
-      const U worst_kept = ~warp_max(kept && score != 0 ? (U)~score : (U)0);
-      const U best_out = warp_max(real && !kept ? score : (U)0);
-      const uint32_t magnitude =
-          max(a != 0 ? magnitude_of(value_of(a)) : 0u, b != 0 ? magnitude_of(value_of(b)) : 0u);
-      const float border = tol.of_sum(magnitude);
-      close = best_out != 0 && value_of(worst_kept) - value_of(best_out) <= border;
-    }
-    if (!kept) {
+    // every lane of a group has its score: to the lane of the group's number
+    const U score = __shfl_sync(0xffffffffu, group_score_of(p, a, b), (lane * span) & 31);
+    const uint32_t magnitude = Tol::kExact ? 0u : max(magnitude_of(a), magnitude_of(b));
+    const uint32_t kept = best_groups(p, lane, score, magnitude, tol, close);
+    if (!((kept >> (lane / span)) & 1u)) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) u[i] = 0;
     }
-    return close;
   }
 
-  // take_best
+  // take_best: lane j notes the j-th key and the lane it came from.
   template <typename Tol>
   LORA_DEV int take(const RouteParams& p, int lane, Tol tol, bool* close) {
-    int id = -1;
-    U prev = 0;
+    U key = 0;
+    int from = 0, place = 0;
     const int rounds = p.top_k + (Tol::kExact ? 0 : 1);
     for (int j = 0; j < rounds; ++j) {
       const U m = warp_max(u[0]);
-      if (m == 0) break;
-      if (!Tol::kExact) {
-        if (prev != 0 && value_of(prev) - value_of(m) <= tol(value_of(prev))) *close = true;
-        prev = m;
-        if (j == p.top_k) break;
+      bool mine = u[0] == m;
+      if (kPlace != kExpert) {
+        const int src = __ffs((int)__ballot_sync(0xffffffffu, mine)) - 1;
+        mine = lane == src;
+        if (kAt) {
+          const int a = __shfl_sync(0xffffffffu, at[0], src);
+          if (lane == j) place = a;
+        }
+        if (lane == j) from = src;
       }
-      const int src = __ffs((int)__ballot_sync(0xffffffffu, u[0] == m)) - 1;
-      int e;
-      if (kPlace == kBeside) e = src * VPL + __shfl_sync(0xffffffffu, at[0], src);
-      else if (kPlace == kLow) e = src * VPL + 15 - (int)(m & 15u);
-      else e = 1023 - (int)(m & 1023u);
-      if (lane == j) id = e;
-      if (lane == src) {
+      if (lane == j) key = m;
+      if (mine) {
 #pragma unroll
         for (int i = 0; i + 1 < VPL; ++i) {
           u[i] = u[i + 1];
-          if (kPlace == kBeside) at[kPlace == kBeside ? i : 0] = at[kPlace == kBeside ? i + 1 : 0];
+          if (kAt) at[kAt ? i : 0] = at[kAt ? i + 1 : 0];
         }
         u[VPL - 1] = 0;
       }
     }
-    return id;
+    if (!Tol::kExact) {
+      // neighbours in the order, the best one left among them (lane top_k; with
+      // top_k = 32 it has no lane: its last neighbour is the list's head)
+      const U before = __shfl_up_sync(0xffffffffu, key, 1);
+      bool near = lane > 0 && lane < rounds && is_open(key) &&
+                  value_of(before) - value_of(key) <= tol(value_of(before));
+      if (rounds > 32) {
+        const U left = warp_max(u[0]);
+        near = near || (lane == 31 && is_open(left) && is_open(key));   // not told: decided in 64 bits
+      }
+      *close |= __any_sync(0xffffffffu, near);
+    }
+    if (lane >= p.top_k || !is_open(key)) return -1;
+    if (kAt) return from * VPL + place;
+    if (kPlace == kLow) return from * VPL + 15 - (int)((uint32_t)key & 15u);
+    return 1023 - (int)((uint32_t)key & 1023u);
   }
 };
 
@@ -408,32 +442,43 @@ struct Sorted {
 // else 0.
 template <int VPL>
 LORA_DEV int group_span(const RouteParams& p) {
+  if (p.num_groups == 1) return 1;
   const int n = p.E / p.num_groups;
   const int span = n / VPL;
   return n % VPL == 0 && (span & (span - 1)) == 0 ? span : 0;
+}
+
+// The selection by keys s + bias, in V.
+template <int VPL, typename V, Place kPlace, typename Tol>
+LORA_DEV int select_by_score(const RouteParams& p, int lane, int span, const float (&x)[VPL],
+                             const V (&s)[VPL], const float (&bias)[VPL], bool finite, Tol tol,
+                             bool* close) {
+  if (VPL <= 8 && span > 0) {
+    Sorted<VPL, V, kPlace> k;
+    make_keys<VPL, V>(x, s, bias, finite, k.u);
+    k.sort(lane);
+    if (p.num_groups > 1) k.keep(p, lane, span, tol, close);
+    return k.take(p, lane, tol, close);
+  }
+  typename KeyOf<V>::U u[VPL];
+  make_keys<VPL, V>(x, s, bias, finite, u);
+  if (p.num_groups > 1) keep_groups(p, lane, u, tol, close);
+  return take_best(p, lane, u, tol, close);
 }
 
 // The same selection in 64 bits, for the tokens whose fp32 keys come too close to
 // tell apart.
 template <int VPL, typename LT>
 __device__ __noinline__ int select_in_double(const RouteParams& p, const LT* row, int lane) {
-  float x[VPL];
+  float x[VPL], bias[VPL];
   double s[VPL];
   bool bad = false, close = false;
-  load_row<VPL, LT>(row, lane, p.E, x, &bad);
-  scores<VPL, double>(p, lane, x, s);
-  const int span = p.num_groups > 1 ? group_span<VPL>(p) : 1;
-  if (VPL <= 8 && span > 0) {
-    Sorted<VPL, double, kBeside> k;
-    make_keys<VPL, double>(p, lane, x, s, k.u, &bad);
-    k.sort(lane);
-    if (p.num_groups > 1) k.keep(p, lane, span, Exact());
-    return k.take(p, lane, Exact(), &close);
-  }
-  uint64_t u[VPL];
-  make_keys<VPL, double>(p, lane, x, s, u, &bad);
-  if (p.num_groups > 1) keep_groups<VPL, double>(p, lane, u, Exact());
-  return take_best<VPL, double>(p, lane, u, Exact(), &close);
+  load_row<VPL, LT>(row, lane, p.E, x);
+  const bool finite = mask_row<VPL>(x, lane * VPL >= p.E, &bad);
+  load_bias<VPL>(p, lane, bias, &bad);
+  scores<VPL, double>(p, x, s);
+  return select_by_score<VPL, double, kBeside>(p, lane, group_span<VPL>(p), x, s, bias, finite,
+                                               Exact(), &close);
 }
 
 // One warp per token.  Without a bias (and without pair scores of groups) the
@@ -445,88 +490,80 @@ __device__ __noinline__ int select_in_double(const RouteParams& p, const LT* row
 template <int VPL, typename LT>
 __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
   const int lane = threadIdx.x & 31;
-  const long long t = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= p.T) return;
-  const LT* row = reinterpret_cast<const LT*>(p.logits) + (size_t)t * p.E;
-  float x[VPL];
-  bool bad = false, close = false;
-  load_row<VPL, LT>(row, lane, p.E, x, &bad);
-  const bool pair = p.num_groups > 1 && p.group_score == LORA_GROUP_TOP_PAIR;
-  const bool by_score = p.bias != nullptr || pair;
-  const int span = p.num_groups > 1 ? group_span<VPL>(p) : 1;
-  int id;
-  float inv_sum = 1.0f, row_max = 0.0f;   // softmax normalisation, where it is needed
-  if (by_score) {
-    float s[VPL];
-    const float smax = scores<VPL, float>(p, lane, x, s);
-    const Within tol = key_error<VPL>(smax);
-    if (VPL <= 8 && span > 0) {
-      Sorted<VPL, float, kLow> k;
-      make_keys<VPL, float>(p, lane, x, s, k.u, &bad);
+  const int warps = (int)(blockDim.x >> 5);
+  const bool by_score =
+      p.bias != nullptr || (p.num_groups > 1 && p.group_score == LORA_GROUP_TOP_PAIR);
+  const int span = group_span<VPL>(p);
+  bool bad = false;
+  float bias[VPL];
+  if (by_score) load_bias<VPL>(p, lane, bias, &bad);
+  for (long long t = (long long)blockIdx.x * warps + (threadIdx.x >> 5); t < p.T;
+       t += (long long)gridDim.x * warps) {
+    const LT* row = reinterpret_cast<const LT*>(p.logits) + (size_t)t * p.E;
+    float x[VPL];
+    bool close = false;
+    load_row<VPL, LT>(row, lane, p.E, x);
+    const bool finite = mask_row<VPL>(x, lane * VPL >= p.E, &bad);
+    int id;
+    if (by_score) {
+      float s[VPL];
+      const float smax = scores<VPL, float>(p, x, s);
+      id = select_by_score<VPL, float, kLow>(p, lane, span, x, s, bias, finite,
+                                             key_error<VPL>(smax), &close);
+      if (close) id = select_in_double<VPL, LT>(p, row, lane);
+    } else if (VPL <= 8 && span > 0) {
+      Sorted<VPL, float, sizeof(LT) == 2 ? kExpert : kBeside> k;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) k.u[i] = order_of(x[i]);
       k.sort(lane);
-      if (p.num_groups > 1) close = k.keep(p, lane, span, tol);
-      id = k.take(p, lane, tol, &close);
+      if (p.num_groups > 1) k.keep(p, lane, span, Exact(), &close);
+      id = k.take(p, lane, Exact(), &close);
     } else {
       uint32_t u[VPL];
-      make_keys<VPL, float>(p, lane, x, s, u, &bad);
-      if (p.num_groups > 1) close = keep_groups<VPL, float>(p, lane, u, tol);
-      id = take_best<VPL, float>(p, lane, u, tol, &close);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) u[i] = order_of(x[i]);
+      if (p.num_groups > 1) keep_groups(p, lane, u, Exact(), &close);
+      id = take_best(p, lane, u, Exact(), &close);
     }
-    if (close) id = select_in_double<VPL, LT>(p, row, lane);
-  } else if (VPL <= 8 && span > 0) {
-    Sorted<VPL, float, sizeof(LT) == 2 ? kExpert : kBeside> k;
+    // weights: lane j has the j-th choice
+    const bool live = id >= 0;
+    const float xs = live ? to_f32(row[id]) : -INFINITY;
+    float w;
+    if (p.renormalize) {
+      // relative to the largest chosen score, so that nothing underflows to 0 / 0
+      const uint32_t mu = warp_max(order_of(xs));
+      const float top = is_open(mu) ? value_of(mu) : 0.0f;
+      if (p.score == LORA_SCORE_SOFTMAX) {
+        w = live ? expf(xs - top) : 0.0f;
+      } else {
+        const float m = fminf(top, 0.0f);
+        w = !live ? 0.0f
+                  : xs >= 0.0f ? 1.0f / (1.0f + expf(-xs)) : expf(xs - m) / (1.0f + expf(xs));
+      }
+      float sum = w;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) k.u[i] = x[i] > -INFINITY ? order_of(x[i]) : 0u;
-    k.sort(lane);
-    if (p.num_groups > 1) k.keep(p, lane, span, Exact());
-    id = k.take(p, lane, Exact(), &close);
-  } else {
-    uint32_t u[VPL];
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      w = live ? w / sum : 0.0f;
+    } else if (p.score == LORA_SCORE_SOFTMAX) {
+      float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) u[i] = x[i] > -INFINITY ? order_of(x[i]) : 0u;
-    if (p.num_groups > 1) keep_groups<VPL, float>(p, lane, u, Exact());
-    id = take_best<VPL, float>(p, lane, u, Exact(), &close);
-  }
-  if (p.score == LORA_SCORE_SOFTMAX && !p.renormalize) {
-    float m = -INFINITY;
+      for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
+      const uint32_t mu = warp_max(order_of(m));
+      m = is_open(mu) ? value_of(mu) : 0.0f;
+      float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) m = fmaxf(m, x[i]);
-    const uint32_t mu = warp_max(m > -INFINITY ? order_of(m) : 0u);
-    row_max = mu != 0u ? value_of(mu) : 0.0f;
-    float sum = 0.0f;
+      for (int i = 0; i < VPL; ++i) sum += expf(x[i] - m);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) sum += expf(x[i] - row_max);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    inv_sum = 1.0f / sum;
-  }
-  // weights: lane j has the j-th choice
-  const bool live = id >= 0;
-  const float xs = live ? to_f32(row[id]) : -INFINITY;
-  float w;
-  if (p.renormalize) {
-    // relative to the largest chosen score, so that nothing underflows to 0 / 0
-    const uint32_t mu = warp_max(live ? order_of(xs) : 0u);
-    const float top = mu != 0u ? value_of(mu) : 0.0f;
-    if (p.score == LORA_SCORE_SOFTMAX) {
-      w = live ? expf(xs - top) : 0.0f;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      w = live ? expf(xs - m) / sum : 0.0f;
     } else {
-      const float m = fminf(top, 0.0f);
-      w = !live ? 0.0f : xs >= 0.0f ? 1.0f / (1.0f + expf(-xs)) : expf(xs - m) / (1.0f + expf(xs));
+      w = live ? 1.0f / (1.0f + expf(-xs)) : 0.0f;
     }
-    float sum = w;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    w = live ? w / sum : 0.0f;
-  } else if (p.score == LORA_SCORE_SOFTMAX) {
-    w = live ? expf(xs - row_max) * inv_sum : 0.0f;
-  } else {
-    w = live ? 1.0f / (1.0f + expf(-xs)) : 0.0f;
-  }
-  if (lane < p.top_k) {
-    const size_t o = (size_t)t * p.top_k + lane;
-    p.ids[o] = id;
-    p.weights[o] = w * p.scale;
+    if (lane < p.top_k) {
+      const size_t o = (size_t)t * p.top_k + lane;
+      p.ids[o] = id;
+      p.weights[o] = w * p.scale;
+    }
   }
   if (p.flags != nullptr && __any_sync(0xffffffffu, bad) && lane == 0)
     raise_flag(p.flags, LORA_FLAG_NONFINITE);
@@ -536,7 +573,9 @@ template <typename LT>
 cudaError_t route_typed(const RouteParams& p, cudaStream_t stream) {
   const int warps = 8;
   const int threads = p.T < warps ? 32 * p.T : 32 * warps;
-  const unsigned grid = (unsigned)(((long long)p.T + warps - 1) / warps);
+  // several tokens a warp where there are many: the biases are loaded once
+  const long long blocks = ((long long)p.T + warps - 1) / warps;
+  const unsigned grid = (unsigned)(blocks < 148 * 8 ? blocks : 148 * 8);
   const int per_lane = (p.E + 31) / 32;
   if (per_lane <= 1) route_kernel<1, LT><<<grid, threads, 0, stream>>>(p);
   else if (per_lane <= 2) route_kernel<2, LT><<<grid, threads, 0, stream>>>(p);
