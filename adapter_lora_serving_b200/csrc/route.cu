@@ -488,7 +488,7 @@ __device__ __noinline__ int select_in_double(const RouteParams& p, const LT* row
 // done again in 64 bits (the filter), so that the chosen experts are those of
 // exact arithmetic.
 template <int VPL, typename LT>
-__global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_kernel(const __grid_constant__ RouteParams p) {
   const int lane = threadIdx.x & 31;
   const int warps = (int)(blockDim.x >> 5);
   const bool by_score =
