@@ -186,25 +186,26 @@ struct Exact {
 };
 // Twice the error of an fp32 key, in units of u = 2^-23.
 //   sigmoid: e^-x moves the score by s (1 - s) (2 + 1.173 |x|) u < u (|x| s (1 - s)
-//     < .23); the sum and the quotient by 3 s u: 4 u of the largest score, 1.
+//     < .23); the sum and the quotient by 3 s u: 4 u in all.
 //   softmax: a term e^z by s (2 + 1.173 |z|) u <= 2.5 u smax (z e^z < .37); the
 //     sum by 2.5 u and half a u for each of VPL + 5 additions, the quotient and the
 //     product by 2.5 u more: (8 + (VPL + 5) / 2) u smax.
 //   the bias sum: half a u of the key; the place within the lane that fills its
-//     lowest bits (Sorted): 8 u at most of it.
+//     four lowest bits (Sorted): 7.5 u of it.
 // A pair's sum has the errors of both its keys, whose magnitudes its own can be
 // far below: `of_sum` has the row's largest.
 struct Within {
   static constexpr bool kExact = false;
   float of_score;
-  LORA_DEV float operator()(float v) const { return of_score + 0x1p-18f * fabsf(v); }
+  LORA_DEV float operator()(float v) const { return of_score + 0x1p-19f * fabsf(v); }
   LORA_DEV float of_sum(uint32_t magnitude) const {
-    return 2.0f * of_score + 0x1p-17f * __uint_as_float(warp_max(magnitude));
+    return 2.0f * of_score + 0x1.1p-18f * __uint_as_float(warp_max(magnitude));
   }
 };
 template <int VPL>
-LORA_DEV Within key_error(float smax) {
-  Within w = {(float)(16 + VPL + 6) * 0x1p-23f * smax};
+LORA_DEV Within key_error(const RouteParams& p, float smax) {
+  Within w;
+  w.of_score = p.score == LORA_SCORE_SIGMOID ? 8.0f * 0x1p-23f : (float)(16 + VPL + 6) * 0x1p-23f * smax;
   return w;
 }
 
@@ -391,52 +392,101 @@ struct Sorted {
     }
   }
 
-  // take_best: lane j notes the j-th key and the lane it came from.
-  template <typename Tol>
-  LORA_DEV int take(const RouteParams& p, int lane, Tol tol, bool* close) {
-    U key = 0;
-    int from = 0, place = 0;
-    const int rounds = p.top_k + (Tol::kExact ? 0 : 1);
-    for (int j = 0; j < rounds; ++j) {
-      const U m = warp_max(u[0]);
-      bool mine = u[0] == m;
-      if (kPlace != kExpert) {
-        const int src = __ffs((int)__ballot_sync(0xffffffffu, mine)) - 1;
-        mine = lane == src;
-        if (kAt) {
-          const int a = __shfl_sync(0xffffffffu, at[0], src);
-          if (lane == j) place = a;
-        }
-        if (lane == j) from = src;
-      }
-      if (lane == j) key = m;
-      if (mine) {
+  // One round: the largest key left and the lane that gives it up (its place, with
+  // kAt, in *place).
+  LORA_DEV U round(int lane, int* from, int* place) {
+    const U m = warp_max(u[0]);
+    bool mine = u[0] == m;
+    if (kPlace != kExpert) {
+      *from = __ffs((int)__ballot_sync(0xffffffffu, mine)) - 1;
+      mine = lane == *from;
+      if (kAt) *place = __shfl_sync(0xffffffffu, at[0], *from);
+    }
+    if (mine) {
 #pragma unroll
-        for (int i = 0; i + 1 < VPL; ++i) {
-          u[i] = u[i + 1];
-          if (kAt) at[kAt ? i : 0] = at[kAt ? i + 1 : 0];
-        }
-        u[VPL - 1] = 0;
+      for (int i = 0; i + 1 < VPL; ++i) {
+        u[i] = u[i + 1];
+        if (kAt) at[kAt ? i : 0] = at[kAt ? i + 1 : 0];
       }
+      u[VPL - 1] = 0;
     }
-    if (!Tol::kExact) {
-      // neighbours in the order, the best one left among them (lane top_k; with
-      // top_k = 32 it has no lane: its last neighbour is the list's head)
-      const U before = __shfl_up_sync(0xffffffffu, key, 1);
-      bool near = lane > 0 && lane < rounds && is_open(key) &&
-                  value_of(before) - value_of(key) <= tol(value_of(before));
-      if (rounds > 32) {
-        const U left = warp_max(u[0]);
-        near = near || (lane == 31 && is_open(left) && is_open(key));   // not told: decided in 64 bits
-      }
-      *close |= __any_sync(0xffffffffu, near);
-    }
-    if (lane >= p.top_k || !is_open(key)) return -1;
+    return m;
+  }
+  LORA_DEV int expert(U key, int from, int place) const {
+    if (!is_open(key)) return -1;
     if (kAt) return from * VPL + place;
     if (kPlace == kLow) return from * VPL + 15 - (int)((uint32_t)key & 15u);
     return 1023 - (int)((uint32_t)key & 1023u);
   }
+
+  // take_best: lane j notes the j-th key and the lane it came from.  Where
+  // neighbours in that order come too close, the next ones are taken too until one
+  // is clear of the last, and `exact` (of a lane's expert) ranks them all; *close
+  // if 32 lanes do not hold them.
+  template <typename Tol, typename ExactKey>
+  LORA_DEV int take(const RouteParams& p, int lane, Tol tol, bool* close, ExactKey exact) {
+    U key = 0;
+    int from = 0, place = 0;
+    int rounds = p.top_k + (Tol::kExact || p.top_k == 32 ? 0 : 1);
+    for (int j = 0; j < rounds; ++j) {
+      int f = 0, a = 0;
+      const U m = round(lane, &f, &a);
+      if (lane == j) {
+        key = m;
+        from = f;
+        place = a;
+      }
+    }
+    int id = expert(key, from, place);
+    if (!Tol::kExact) {
+      const U before = __shfl_up_sync(0xffffffffu, key, 1);
+      const bool near = lane > 0 && lane < rounds && id >= 0 &&
+                        value_of(before) - value_of(key) <= tol(value_of(before));
+      if (__any_sync(0xffffffffu, near)) {
+        U last = __shfl_sync(0xffffffffu, key, rounds - 1);
+        while (true) {
+          const U next = warp_max(u[0]);
+          if (!is_open(next) || value_of(last) - value_of(next) > tol(value_of(last))) break;
+          if (rounds == 32) {
+            *close = true;
+            break;
+          }
+          int f = 0, a = 0;
+          last = round(lane, &f, &a);
+          if (lane == rounds) id = expert(last, f, a);
+          ++rounds;
+        }
+        if (!*close) {
+          const auto mine = exact(id);
+          int rank = 0;
+          for (int j = 0; j < rounds; ++j) {
+            const auto other = __shfl_sync(0xffffffffu, mine, j);
+            const int e = __shfl_sync(0xffffffffu, id, j);
+            rank += e >= 0 && (other > mine || (other == mine && e < id)) ? 1 : 0;
+          }
+          if (id < 0 || lane >= rounds) rank = 32;
+          int sorted = -1;
+          for (int j = 0; j < p.top_k; ++j) {
+            const uint32_t who = __ballot_sync(0xffffffffu, rank == j);
+            const int e = __shfl_sync(0xffffffffu, id, who != 0 ? __ffs((int)who) - 1 : 0);
+            if (lane == j && who != 0) sorted = e;
+          }
+          id = sorted;
+        }
+      } else if (p.top_k == 32) {
+        // no lane for the best one left
+        const U next = warp_max(u[0]), last = __shfl_sync(0xffffffffu, key, 31);
+        if (is_open(next) && value_of(last) - value_of(next) <= tol(value_of(last))) *close = true;
+      }
+    }
+    return lane < p.top_k ? id : -1;
+  }
 };
+
+// The exact key of expert e of a row, for a few experts whose fp32 keys are close:
+// every lane its own e (or -1), the whole warp together.
+template <int VPL, typename LT>
+__device__ __noinline__ double exact_key(const RouteParams& p, const LT* row, int lane, int e);
 
 // Lanes per expert group where groups are whole lanes, a power of two of them;
 // else 0.
@@ -449,21 +499,47 @@ LORA_DEV int group_span(const RouteParams& p) {
 }
 
 // The selection by keys s + bias, in V.
-template <int VPL, typename V, Place kPlace, typename Tol>
+template <int VPL, typename V, Place kPlace, typename Tol, typename ExactKey>
 LORA_DEV int select_by_score(const RouteParams& p, int lane, int span, const float (&x)[VPL],
                              const V (&s)[VPL], const float (&bias)[VPL], bool finite, Tol tol,
-                             bool* close) {
+                             bool* close, ExactKey exact) {
   if (VPL <= 8 && span > 0) {
     Sorted<VPL, V, kPlace> k;
     make_keys<VPL, V>(x, s, bias, finite, k.u);
     k.sort(lane);
     if (p.num_groups > 1) k.keep(p, lane, span, tol, close);
-    return k.take(p, lane, tol, close);
+    if (*close) return -1;
+    return k.take(p, lane, tol, close, exact);
   }
   typename KeyOf<V>::U u[VPL];
   make_keys<VPL, V>(x, s, bias, finite, u);
   if (p.num_groups > 1) keep_groups(p, lane, u, tol, close);
   return take_best(p, lane, u, tol, close);
+}
+
+struct NoKey {
+  LORA_DEV double operator()(int) const { return 0.0; }
+};
+
+template <int VPL, typename LT>
+__device__ __noinline__ double exact_key(const RouteParams& p, const LT* row, int lane, int e) {
+  const double x = e >= 0 ? (double)to_f32(row[e]) : 0.0;
+  const double b = e >= 0 && p.bias != nullptr ? (double)__ldg(p.bias + e) : 0.0;
+  if (p.score == LORA_SCORE_SIGMOID) return 1.0 / (1.0 + exp(-x)) + b;
+  float v[VPL];
+  bool bad = false;
+  load_row<VPL, LT>(row, lane, p.E, v);
+  mask_row<VPL>(v, lane * VPL >= p.E, &bad);
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) m = fmaxf(m, v[i]);
+  m = value_of(warp_max(order_of(m)));   // finite: there are keys to compare
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) sum += exp((double)v[i] - (double)m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return exp(x - (double)m) / sum + b;
 }
 
 // The same selection in 64 bits, for the tokens whose fp32 keys come too close to
@@ -478,7 +554,7 @@ __device__ __noinline__ int select_in_double(const RouteParams& p, const LT* row
   load_bias<VPL>(p, lane, bias, &bad);
   scores<VPL, double>(p, x, s);
   return select_by_score<VPL, double, kBeside>(p, lane, group_span<VPL>(p), x, s, bias, finite,
-                                               Exact(), &close);
+                                               Exact(), &close, NoKey());
 }
 
 // One warp per token.  Without a bias (and without pair scores of groups) the
@@ -509,7 +585,9 @@ __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_k
       float s[VPL];
       const float smax = scores<VPL, float>(p, x, s);
       id = select_by_score<VPL, float, kLow>(p, lane, span, x, s, bias, finite,
-                                             key_error<VPL>(smax), &close);
+                                             key_error<VPL>(p, smax), &close, [&](int e) {
+                                               return exact_key<VPL, LT>(p, row, lane, e);
+                                             });
       if (close) id = select_in_double<VPL, LT>(p, row, lane);
     } else if (VPL <= 8 && span > 0) {
       Sorted<VPL, float, sizeof(LT) == 2 ? kExpert : kBeside> k;
@@ -517,7 +595,7 @@ __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_k
       for (int i = 0; i < VPL; ++i) k.u[i] = order_of(x[i]);
       k.sort(lane);
       if (p.num_groups > 1) k.keep(p, lane, span, Exact(), &close);
-      id = k.take(p, lane, Exact(), &close);
+      id = k.take(p, lane, Exact(), &close, NoKey());
     } else {
       uint32_t u[VPL];
 #pragma unroll
