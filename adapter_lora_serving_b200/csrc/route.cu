@@ -665,17 +665,13 @@ cudaError_t route_typed(const RouteParams& p, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// Grouping: a stable counting sort of the pairs by expert, in one launch of
-// one thread-block cluster.  CTA c takes the c-th run of pairs and warp w of it
-// the w-th share of that run, so (CTA, warp, position) order is pair order.
+// Grouping: a stable counting sort of the pairs by expert.
+// Few pairs: one CTA of NT threads.  Warp w takes the w-th share of the pairs, so
+// (warp, position) order is pair order.
 //   1. every warp counts its pairs per expert (in its own table: no atomics);
-//   2. per expert, a prefix over the warps, then over the CTAs' totals through
-//      distributed shared memory, then over the experts;
+//   2. per expert, a prefix over the warps, then over the experts;
 //   3. every warp walks its pairs again and hands out rows.
 // ---------------------------------------------------------------------------
-
-constexpr int kGrThreads = 1024;
-constexpr int kGrWarps = kGrThreads / 32;
 
 LORA_DEV int pair_expert(const GroupParams& p, int i, int end, bool* bad) {
   int e = -1;
@@ -689,78 +685,93 @@ LORA_DEV int pair_expert(const GroupParams& p, int i, int end, bool* bad) {
   return e;
 }
 
-__global__ void __launch_bounds__(kGrThreads, 1) group_kernel(const GroupParams p) {
-  extern __shared__ int gr_smem[];
-  __shared__ int scratch[kGrWarps];
-  int* total = gr_smem;             // [E]: this CTA's pairs per expert
-  int* table = gr_smem + p.E;       // [kGrWarps][E]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ctas = (int)gridDim.x, rank = (int)blockIdx.x;
-  // shares in whole warps' steps
-  const int steps = (p.n + 32 * kGrWarps * ctas - 1) / (32 * kGrWarps * ctas);
-  const long long first = ((long long)rank * kGrWarps + warp) * steps * 32;
-  const int begin = (int)min(first, (long long)p.n);
-  const int end = (int)min(first + (long long)steps * 32, (long long)p.n);
-  int* mine = table + warp * p.E;
+// Counts a warp's pairs [begin, end) in its table.
+LORA_DEV void count_share(const GroupParams& p, int begin, int end, int* mine, bool* bad) {
+  const int lane = threadIdx.x & 31;
   for (int e = lane; e < p.E; e += 32) mine[e] = 0;
   __syncwarp();
+  for (int i0 = begin; i0 < end; i0 += 128) {
+    int e[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) e[q] = pair_expert(p, i0 + 32 * q + lane, end, bad);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (i0 + 32 * q >= end) break;
+      const uint32_t same = __match_any_sync(0xffffffffu, e[q]);
+      if (e[q] >= 0 && lane == __ffs((int)same) - 1) mine[e[q]] += __popc(same);
+      __syncwarp();
+    }
+  }
+}
+
+// Hands out the rows of a warp's pairs, from its table of first rows.
+LORA_DEV void place_share(const GroupParams& p, int begin, int end, int* mine) {
+  const int lane = threadIdx.x & 31;
   bool bad = false;
-  for (int i0 = begin; i0 < end; i0 += 32) {
-    const int e = pair_expert(p, i0 + lane, end, &bad);
-    const uint32_t same = __match_any_sync(0xffffffffu, e);
-    if (e >= 0 && lane == __ffs((int)same) - 1) mine[e] += __popc(same);
-    __syncwarp();
-  }
-  if (p.flags != nullptr && __any_sync(0xffffffffu, bad) && lane == 0)
-    raise_flag(p.flags, LORA_FLAG_BAD_EXPERT);
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kGrThreads) {
-    int run = 0;
-    for (int w = 0; w < kGrWarps; ++w) {
-      const int c = table[w * p.E + e];
-      table[w * p.E + e] = run;
-      run += c;
-    }
-    total[e] = run;
-  }
-  cluster_sync();
-  // kRouteMaxExperts == kGrThreads: one expert per thread
-  const int e = threadIdx.x;
-  int before = 0, all = 0;
-  if (e < p.E) {
-    for (int c = 0; c < ctas; ++c) {
-      const int t = dsmem_ld_s32(dsmem_addr(total + e, (uint32_t)c));
-      if (c < rank) before += t;
-      all += t;
-    }
-  }
-  int rows = 0;
-  const int incl = block_inclusive_scan<kGrThreads>(all, scratch, &rows);
-  if (e < p.E) {
-    const int base = incl - all;
-    if (rank == 0) p.expert_offsets[e] = base;
-    for (int w = 0; w < kGrWarps; ++w) table[w * p.E + e] += base + before;
-  }
-  if (rank == 0 && threadIdx.x == 0) p.expert_offsets[p.E] = rows;
-  cluster_sync();   // also: no CTA leaves while its totals are read
-  for (int i0 = begin; i0 < end; i0 += 32) {
-    const int i = i0 + lane;
-    const int ex = pair_expert(p, i, end, &bad);
-    const uint32_t same = __match_any_sync(0xffffffffu, ex);
-    int row = -1;
-    if (ex >= 0) row = mine[ex] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (ex >= 0 && lane == __ffs((int)same) - 1) mine[ex] += __popc(same);
-    __syncwarp();
-    if (i < end) {
-      p.pair_row[i] = row;
-      if (row >= 0) {
-        const int t = i / p.top_k;
-        p.row_token[row] = t;
-        if (p.row_slot != nullptr) p.row_slot[row] = __ldg(p.token_slot + t);
+  for (int i0 = begin; i0 < end; i0 += 128) {
+    int e[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) e[q] = pair_expert(p, i0 + 32 * q + lane, end, &bad);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int i = i0 + 32 * q + lane;
+      if (i0 + 32 * q >= end) break;
+      const uint32_t same = __match_any_sync(0xffffffffu, e[q]);
+      int row = -1;
+      if (e[q] >= 0) row = mine[e[q]] + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (e[q] >= 0 && lane == __ffs((int)same) - 1) mine[e[q]] += __popc(same);
+      __syncwarp();
+      if (i < end) {
+        p.pair_row[i] = row;
+        if (row >= 0) {
+          const int t = i / p.top_k;
+          p.row_token[row] = t;
+          if (p.row_slot != nullptr) p.row_slot[row] = __ldg(p.token_slot + t);
+        }
       }
     }
   }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(NT) group_small_kernel(const GroupParams p) {
+  constexpr int kWarps = NT / 32;
+  extern __shared__ int gr_smem[];   // [kWarps][E]
+  __shared__ int scratch[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.n + NT - 1) / NT * 32;   // whole warps' steps
+  const int begin = min(warp * per, p.n), end = min(begin + per, p.n);
+  int* mine = gr_smem + warp * p.E;
+  bool bad = false;
+  count_share(p, begin, end, mine, &bad);
+  if (p.flags != nullptr && __any_sync(0xffffffffu, bad) && lane == 0)
+    raise_flag(p.flags, LORA_FLAG_BAD_EXPERT);
+  __syncthreads();
+  int carry = 0;
+  for (int e0 = 0; e0 < p.E; e0 += NT) {
+    const int e = e0 + (int)threadIdx.x;
+    int total = 0;
+    if (e < p.E) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const int c = gr_smem[w * p.E + e];
+        gr_smem[w * p.E + e] = total;
+        total += c;
+      }
+    }
+    int rows = 0;
+    const int first = carry + block_inclusive_scan<NT>(total, scratch, &rows) - total;
+    carry += rows;
+    if (e < p.E) {
+      p.expert_offsets[e] = first;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) gr_smem[w * p.E + e] += first;
+    }
+  }
+  if (threadIdx.x == 0) p.expert_offsets[p.E] = carry;
+  __syncthreads();
+  place_share(p, begin, end, mine);
 }
 
 // Many pairs: three launches over all SMs, without a workspace.  pair_row is
@@ -772,6 +783,7 @@ __global__ void __launch_bounds__(kGrThreads, 1) group_kernel(const GroupParams 
 //      into expert_offsets;
 //   3. place: a CTA takes its table, ranks its run and writes the rows.
 
+constexpr int kSmallPairs = 2048;   // one CTA up to here (7.4 us; three launches 7.5 at 4096)
 constexpr int kRunThreads = 512;
 constexpr int kRunWarps = kRunThreads / 32;
 
@@ -782,24 +794,6 @@ struct Runs {
 LORA_DEV void run_bounds(const GroupParams& p, const Runs& r, int b, int* begin, int* end) {
   *begin = b * r.length;
   *end = b + 1 == r.count ? p.n : (b + 1) * r.length;
-}
-
-// Warp w's share of a run, and its table of pairs per expert.
-LORA_DEV void count_share(const GroupParams& p, int begin, int end, int* mine, bool* bad) {
-  const int lane = threadIdx.x & 31;
-  for (int e = lane; e < p.E; e += 32) mine[e] = 0;
-  __syncwarp();
-  for (int i0 = begin; i0 < end; i0 += 128) {
-    int e[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) e[q] = pair_expert(p, i0 + 32 * q + lane, end, bad);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t same = __match_any_sync(0xffffffffu, e[q]);
-      if (e[q] >= 0 && lane == __ffs((int)same) - 1) mine[e[q]] += __popc(same);
-      __syncwarp();
-    }
-  }
 }
 
 LORA_DEV void share_of(int begin, int end, int* lo, int* hi) {
@@ -880,7 +874,7 @@ __global__ void __launch_bounds__(kScanThreads) group_scan_kernel(const GroupPar
 
 __global__ void __launch_bounds__(kRunThreads) group_place_kernel(const GroupParams p, const Runs r) {
   extern __shared__ int gr_smem[];   // [kRunWarps][E]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5;
   int begin, end, lo, hi;
   run_bounds(p, r, (int)blockIdx.x, &begin, &end);
   share_of(begin, end, &lo, &hi);
@@ -898,29 +892,7 @@ __global__ void __launch_bounds__(kRunThreads) group_place_kernel(const GroupPar
     }
   }
   __syncthreads();
-  for (int i0 = lo; i0 < hi; i0 += 128) {
-    int ex[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) ex[q] = pair_expert(p, i0 + 32 * q + lane, hi, &bad);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int i = i0 + 32 * q + lane;
-      const uint32_t same = __match_any_sync(0xffffffffu, ex[q]);
-      int row = -1;
-      if (ex[q] >= 0) row = mine[ex[q]] + __popc(same & ((1u << lane) - 1u));
-      __syncwarp();
-      if (ex[q] >= 0 && lane == __ffs((int)same) - 1) mine[ex[q]] += __popc(same);
-      __syncwarp();
-      if (i < hi) {
-        p.pair_row[i] = row;
-        if (row >= 0) {
-          const int t = i / p.top_k;
-          p.row_token[row] = t;
-          if (p.row_slot != nullptr) p.row_slot[row] = __ldg(p.token_slot + t);
-        }
-      }
-    }
-  }
+  place_share(p, lo, hi, mine);
 }
 
 template <typename K>
@@ -1004,6 +976,12 @@ cudaError_t combine_typed(const CombineParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <int NT>
+cudaError_t group_small(const GroupParams& p, cudaStream_t stream) {
+  group_small_kernel<NT><<<1, NT, (size_t)(NT / 32) * p.E * 4, stream>>>(p);
+  return cudaGetLastError();
+}
+
 std::mutex g_mu;
 bool g_group_attr[64];
 
@@ -1023,43 +1001,27 @@ cudaError_t group_launch(const GroupParams& p, cudaStream_t stream) {
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (!g_group_attr[dev]) {
-      err = cudaFuncSetAttribute(group_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kGrWarps + 1) * kRouteMaxExperts * 4);
-      if (err != cudaSuccess) return err;
-      err = cudaFuncSetAttribute(group_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kRunWarps * kRouteMaxExperts * 4);
+      const int smem = kRunWarps * kRouteMaxExperts * 4;   // 64 KB
+      err = cudaFuncSetAttribute(group_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(group_small_kernel<512>,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
       if (err != cudaSuccess) return err;
       g_group_attr[dev] = true;
     }
   }
-  if (p.n > 16384) {
-    Runs r;
-    r.length = p.E > 1024 ? p.E : 1024;
-    while (p.n / r.length > 592) r.length *= 2;
-    r.count = p.n / r.length;
-    err = launch_after(group_count_kernel, r.count, kRunThreads, (size_t)p.E * 4, false, stream, p, r);
-    if (err != cudaSuccess) return err;
-    err = launch_after(group_scan_kernel, 1, kScanThreads, 0, true, stream, p, r);
-    if (err != cudaSuccess) return err;
-    return launch_after(group_place_kernel, r.count, kRunThreads, (size_t)kRunWarps * p.E * 4, true,
-                        stream, p, r);
-  }
-  // one CTA per 4096 pairs, up to a cluster of eight
-  int ctas = 1;
-  while (ctas < 8 && (long long)ctas * 4096 < p.n) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  cfg.gridDim = dim3((unsigned)ctas, 1, 1);
-  cfg.blockDim = dim3(kGrThreads, 1, 1);
-  cfg.dynamicSmemBytes = (size_t)(kGrWarps + 1) * p.E * 4;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, group_kernel, p);
+  if (p.n <= 512) return group_small<128>(p, stream);
+  if (p.n <= kSmallPairs) return group_small<512>(p, stream);
+  Runs r;
+  r.length = p.E > 1024 ? p.E : 1024;
+  while (p.n / r.length > 592) r.length *= 2;
+  r.count = p.n / r.length;
+  err = launch_after(group_count_kernel, r.count, kRunThreads, (size_t)p.E * 4, false, stream, p, r);
+  if (err != cudaSuccess) return err;
+  err = launch_after(group_scan_kernel, 1, kScanThreads, 0, true, stream, p, r);
+  if (err != cudaSuccess) return err;
+  return launch_after(group_place_kernel, r.count, kRunThreads, (size_t)kRunWarps * p.E * 4, true,
+                      stream, p, r);
 }
 
 cudaError_t combine_launch(const CombineParams& p, int type, cudaStream_t stream) {
