@@ -9,6 +9,8 @@
 // Memory bound: a value is read once (bf16: 2 bytes) and half a byte and 1/32
 // byte written; a thread owns eight consecutive values (one 16-byte load), four
 // threads a block, four such pieces in flight per thread.
+#include <type_traits>
+
 #include "elem.cuh"
 #include "experts.h"
 
@@ -37,104 +39,153 @@ LORA_DEV uint32_t pack_e2m1(const float (&v)[8]) {
   return r;
 }
 
-__device__ __noinline__ double silu_mul_double(float g, float u) {
-  return (double)g / (1.0 + exp(-(double)g)) * (double)u;
-}
-
-// silu(g) * u rounded once to T.  The fp32 value is within 2^-21 of it (expf,
-// a sum, a division and a product) unless the exponential is near its overflow
-// or the result near underflow; where moving it by 2^-20 changes what it rounds
-// to, it is computed again in 64 bits.
+// Largest magnitude of eight values, as ordered bits, and those bits as fp32's.
+// 16-bit types compare two at a time.
 template <typename T>
-LORA_DEV T silu_mul(float g, float u) {
+struct Top {
+  static LORA_DEV uint32_t of(const Raw8<T>& r) {
+    const uint32_t k = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(r.v.x & k, r.v.y & k), __vmaxu2(r.v.z & k, r.v.w & k));
+    return max(m & 0xffffu, m >> 16);
+  }
+  static LORA_DEV uint32_t as_f32(uint32_t m) {
+    return __float_as_uint(unpack2(T(), m).x);
+  }
+};
+template <>
+struct Top<float> {
+  static LORA_DEV uint32_t of(const Raw8<float>& r) {
+    float f[8];
+    r.get(f);
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(f[k]) & 0x7fffffffu);
+    return m;
+  }
+  static LORA_DEV uint32_t as_f32(uint32_t m) { return m; }
+};
+
+// silu(g) * u rounded once to T.  In fp32 (expf, a sum, a fast quotient, a product)
+// it is within 8 ulps; where that lets it fall on either side of a rounding border
+// of T (the middle of the bits that T drops), or the exponential or the result is
+// near the end of fp32's range, or T is subnormal, it is computed again in 64 bits.
+// Returns whether it is decided, in *out.
+template <typename T>
+LORA_DEV bool silu_mul_fast(float g, float u, float* out) {
+  constexpr bool kBf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
+  constexpr uint32_t kDropped = kBf16 ? 0xffffu : 0x1fffu, kMiddle = kBf16 ? 0x8000u : 0x1000u;
   const float e = expf(-g);
-  const float a = g / (1.0f + e) * u;
-  const T lo = from_f32<T>(a * (1.0f - 0x1p-20f)), hi = from_f32<T>(a * (1.0f + 0x1p-20f));
-  if (to_f32(lo) == to_f32(hi) && e < 0x1p100f && fabsf(a) > 0x1p-100f) return lo;
-  const double d = silu_mul_double(g, u);
-  // double -> fp32 -> T would round twice: fold what the first step drops into
-  // the last bit (round to odd), below every rounding border of T
-  const float f = (float)d;
-  const double back = (double)f;
-  if (back == d || !(fabs(d) < (double)INFINITY)) return from_f32<T>(f);
-  uint32_t b = __float_as_uint(f);
-  if (fabs(back) > fabs(d)) b -= 1u;   // towards zero
-  return from_f32<T>(__uint_as_float(b | 1u));
+  const float a = __fdividef(g, 1.0f + e) * u;
+  *out = a;
+  const bool clear = ((__float_as_uint(a) - kMiddle + 16u) & kDropped) > 32u;
+  return clear && e < 0x1p100f && fabsf(a) > (kBf16 ? 0x1p-100f : 0x1p-14f) && fabsf(a) < 0x1p126f;
 }
 template <>
-LORA_DEV float silu_mul<float>(float g, float u) { return (float)silu_mul_double(g, u); }
+LORA_DEV bool silu_mul_fast<float>(float, float, float*) { return false; }
+
+// The same from 64 bits: double -> fp32 -> T would round twice, so what the first
+// step drops is folded into the last bit (round to odd), below T's borders.
+template <typename T>
+__device__ __noinline__ float silu_mul_exact(float g, float u) {
+  const double d = (double)g / (1.0 + exp(-(double)g)) * (double)u;
+  const float f = (float)d;
+  const double back = (double)f;
+  if (sizeof(T) == 4 || back == d || !(fabs(d) < (double)INFINITY)) return f;
+  uint32_t b = __float_as_uint(f);
+  if (fabs(back) > fabs(d)) b -= 1u;   // towards zero
+  return __uint_as_float(b | 1u);
+}
+
+// i / d for i < 2^31 by a multiplication (d >= 1): the high word of i * m, shifted.
+struct Divisor {
+  uint32_t d, m, shift;
+  __host__ explicit Divisor(uint32_t div) : d(div), m(0), shift(0) {
+    // shift = ceil(log2 d), m = ceil(2^(31 + shift) / d): exact for 31-bit i
+    while ((1ull << shift) < div) ++shift;
+    m = (uint32_t)(((1ull << (31 + shift)) + div - 1) / div);
+  }
+  LORA_DEV uint32_t operator()(uint32_t i) const {
+    return (uint32_t)(((uint64_t)i * m) >> 31 >> shift);
+  }
+};
 
 template <typename T, bool kSilu>
-__global__ void __launch_bounds__(kQThreads) mx_quant_kernel(const MxQuantParams p) {
-  const int cols = p.F >> 3;   // pieces per row, a multiple of four
-  const int rows = p.row_count != nullptr ? min(max(__ldg(p.row_count), 0), p.rows) : p.rows;
-  const long long n = (long long)rows * cols;
+__global__ void __launch_bounds__(kQThreads)
+mx_quant_kernel(const __grid_constant__ MxQuantParams p, const Divisor by_cols, int first_row) {
+  // rows [first_row, first_row + the launch's); fewer than 2^31 pieces
+  const int total = p.row_count != nullptr ? min(max(__ldg(p.row_count), 0), p.rows) : p.rows;
+  const uint32_t cols = by_cols.d;   // pieces per row, a multiple of four
+  const uint32_t rows = (uint32_t)min(max(total - first_row, 0), (int)(0x7fffffffu / cols));
+  const uint32_t n = rows * cols;
   const T* x = reinterpret_cast<const T*>(p.x);
-  const int pitch = kSilu ? 2 * p.F : p.F;
+  const size_t pitch = kSilu ? 2 * (size_t)p.F : (size_t)p.F;
   const int lane = threadIdx.x & 31;
   bool bad_row = false, bad_val = false;
-  for (long long i0 = (long long)blockIdx.x * kQThreads * kQPieces; i0 < n;
-       i0 += (long long)gridDim.x * kQThreads * kQPieces) {
+  const uint32_t step = gridDim.x * (kQThreads * kQPieces);
+  for (uint32_t i0 = blockIdx.x * (kQThreads * kQPieces); i0 < n; i0 += step) {
     Raw8<T> v[kQPieces], w[kSilu ? kQPieces : 1];
     bool live[kQPieces];
-    int row[kQPieces], col[kQPieces];
+    size_t at[kQPieces];
 #pragma unroll
     for (int q = 0; q < kQPieces; ++q) {
-      const long long i = i0 + q * kQThreads + threadIdx.x;
+      const uint32_t i = i0 + q * kQThreads + threadIdx.x;
       live[q] = i < n;
-      row[q] = 0;
-      col[q] = 0;
+      at[q] = 0;
       if (live[q]) {
-        row[q] = (int)(i / cols);
-        col[q] = (int)(i - (long long)row[q] * cols) * 8;
-        int src = row[q];
-        if (p.row_index != nullptr) src = __ldg(p.row_index + row[q]);
+        const uint32_t r = by_cols(i);
+        const uint32_t c = (i - r * cols) * 8;
+        const int row = first_row + (int)r;
+        int src = row;
+        if (p.row_index != nullptr) src = __ldg(p.row_index + row);
+        at[q] = (size_t)row * p.F + c;
         if (src < 0 || src >= p.x_rows) {
           bad_row = true;
           live[q] = false;
         } else {
-          v[q].load(x + (size_t)src * pitch + col[q]);
-          if (kSilu) w[q].load(x + (size_t)src * pitch + p.F + col[q]);
+          v[q].load(x + (size_t)src * pitch + c);
+          if (kSilu) w[q].load(x + (size_t)src * pitch + p.F + c);
         }
       }
     }
 #pragma unroll
     for (int q = 0; q < kQPieces; ++q) {
-      float f[8];
       uint32_t top = 0;
       if (live[q]) {
-        v[q].get(f);
         if (kSilu) {
-          float u[8];
+          float g[8], u[8], a[8];
+          v[q].get(g);
           w[q].get(u);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = to_f32(silu_mul<T>(f[k], u[k]));
-          v[q].set(f);
+          for (int k = 0; k < 8; ++k)
+            if (!silu_mul_fast<T>(g[k], u[k], &a[k])) a[k] = silu_mul_exact<T>(g[k], u[k]);
+          v[q].set(a);
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[k]) & 0x7fffffffu);
+        top = Top<T>::of(v[q]);
       }
       // the four threads of a block are neighbours and live or dead together
       __syncwarp();
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      if (!live[q]) continue;
-      const bool finite = top < 0x7f800000u;
-      const uint32_t ex = top >> 23;                       // biased exponent, 0 if subnormal
-      const uint32_t scale = finite ? (ex > 2u ? ex - 2u : 0u) : 255u;
-      // 2^-(scale - 127): a normal number for every scale a finite block has
-      const float inv = finite ? __uint_as_float((254u - scale) << 23) : 0.0f;
+      if (live[q]) {
+        const uint32_t bits = Top<T>::as_f32(top);
+        const bool finite = bits < 0x7f800000u;
+        const uint32_t ex = bits >> 23;                      // biased exponent, 0 if subnormal
+        const uint32_t scale = finite ? (ex > 2u ? ex - 2u : 0u) : 255u;
+        // 2^-(scale - 127): a normal number for every scale a finite block has
+        const float inv = finite ? __uint_as_float((254u - scale) << 23) : 0.0f;
+        float f[8];
+        v[q].get(f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= inv;
-      uint32_t codes = pack_e2m1(f);
-      if (!finite) {
-        codes = 0;
-        bad_val = true;
+        for (int k = 0; k < 8; ++k) f[k] *= inv;
+        uint32_t codes = pack_e2m1(f);
+        if (!finite) {
+          codes = 0;
+          bad_val = true;
+        }
+        *reinterpret_cast<uint32_t*>(p.codes + (at[q] >> 1)) = codes;
+        if ((lane & 3) == 0) p.scales[at[q] >> 5] = (uint8_t)scale;
+        if (p.rows_out != nullptr) v[q].store(reinterpret_cast<T*>(p.rows_out) + at[q]);
       }
-      const size_t at = (size_t)row[q] * p.F + col[q];
-      *reinterpret_cast<uint32_t*>(p.codes + (at >> 1)) = codes;
-      if ((lane & 3) == 0) p.scales[at >> 5] = (uint8_t)scale;
-      if (p.rows_out != nullptr) v[q].store(reinterpret_cast<T*>(p.rows_out) + at);
     }
   }
   if (p.flags != nullptr) {
@@ -190,9 +241,16 @@ int grid_for(long long n, int per_block) {
 
 template <typename T>
 cudaError_t quant_typed(const MxQuantParams& p, int act, cudaStream_t stream) {
-  const int grid = grid_for((long long)p.rows * (p.F >> 3), kQThreads * kQPieces);
-  if (act == LORA_ACT_SILU_MUL) mx_quant_kernel<T, true><<<grid, kQThreads, 0, stream>>>(p);
-  else mx_quant_kernel<T, false><<<grid, kQThreads, 0, stream>>>(p);
+  const Divisor by_cols((uint32_t)p.F >> 3);
+  const int most = (int)(0x7fffffffu / by_cols.d);   // rows of one launch
+  for (long long first = 0; first < p.rows; first += most) {
+    const long long rows = p.rows - first < most ? p.rows - first : most;
+    const int grid = grid_for(rows * by_cols.d, kQThreads * kQPieces);
+    if (act == LORA_ACT_SILU_MUL)
+      mx_quant_kernel<T, true><<<grid, kQThreads, 0, stream>>>(p, by_cols, (int)first);
+    else
+      mx_quant_kernel<T, false><<<grid, kQThreads, 0, stream>>>(p, by_cols, (int)first);
+  }
   return cudaGetLastError();
 }
 
