@@ -7,8 +7,7 @@
 // (NaN) and codes 0, and the caller's flag is raised.
 //
 // Memory bound: a value is read once (bf16: 2 bytes) and half a byte and 1/32
-// byte written; a thread owns eight consecutive values (one 16-byte load), four
-// threads a block, four such pieces in flight per thread.
+// byte written.
 #include <type_traits>
 
 #include "elem.cuh"
@@ -96,6 +95,17 @@ __device__ __noinline__ float silu_mul_exact(float g, float u) {
   return __uint_as_float(b | 1u);
 }
 
+// What a thread takes at once: 16 values of a 16-bit type (two of them per block,
+// less to do per value besides the conversions, which bound the kernel: 39 us with
+// eight for 16384 x 4096 bf16), eight of fp32; and how many such pieces are in
+// flight.
+template <typename T>
+struct Piece {
+  static constexpr int kVals = sizeof(T) == 2 ? 16 : 8;
+  template <bool kSilu>
+  static constexpr int count() { return kSilu ? 1 : 2; }
+};
+
 // i / d for i < 2^31 by a multiplication (d >= 1): the high word of i * m, shifted.
 struct Divisor {
   uint32_t d, m, shift;
@@ -112,28 +122,30 @@ struct Divisor {
 template <typename T, bool kSilu>
 __global__ void __launch_bounds__(kQThreads)
 mx_quant_kernel(const __grid_constant__ MxQuantParams p, const Divisor by_cols, int first_row) {
+  constexpr int kVals = Piece<T>::kVals, kRaw = kVals / 8;
+  constexpr int kPieces = Piece<T>::template count<kSilu>();
   // rows [first_row, first_row + the launch's); fewer than 2^31 pieces
   const int total = p.row_count != nullptr ? min(max(__ldg(p.row_count), 0), p.rows) : p.rows;
-  const uint32_t cols = by_cols.d;   // pieces per row, a multiple of four
+  const uint32_t cols = by_cols.d;   // pieces per row: whole blocks
   const uint32_t rows = (uint32_t)min(max(total - first_row, 0), (int)(0x7fffffffu / cols));
   const uint32_t n = rows * cols;
   const T* x = reinterpret_cast<const T*>(p.x);
   const size_t pitch = kSilu ? 2 * (size_t)p.F : (size_t)p.F;
   const int lane = threadIdx.x & 31;
   bool bad_row = false, bad_val = false;
-  const uint32_t step = gridDim.x * (kQThreads * kQPieces);
-  for (uint32_t i0 = blockIdx.x * (kQThreads * kQPieces); i0 < n; i0 += step) {
-    Raw8<T> v[kQPieces], w[kSilu ? kQPieces : 1];
-    bool live[kQPieces];
-    size_t at[kQPieces];
+  const uint32_t step = gridDim.x * (kQThreads * kPieces);
+  for (uint32_t i0 = blockIdx.x * (kQThreads * kPieces); i0 < n; i0 += step) {
+    Raw8<T> v[kPieces][kRaw], w[kSilu ? kPieces : 1][kRaw];
+    bool live[kPieces];
+    size_t at[kPieces];
 #pragma unroll
-    for (int q = 0; q < kQPieces; ++q) {
+    for (int q = 0; q < kPieces; ++q) {
       const uint32_t i = i0 + q * kQThreads + threadIdx.x;
       live[q] = i < n;
       at[q] = 0;
       if (live[q]) {
         const uint32_t r = by_cols(i);
-        const uint32_t c = (i - r * cols) * 8;
+        const uint32_t c = (i - r * cols) * kVals;
         const int row = first_row + (int)r;
         int src = row;
         if (p.row_index != nullptr) src = __ldg(p.row_index + row);
@@ -142,30 +154,37 @@ mx_quant_kernel(const __grid_constant__ MxQuantParams p, const Divisor by_cols, 
           bad_row = true;
           live[q] = false;
         } else {
-          v[q].load(x + (size_t)src * pitch + c);
-          if (kSilu) w[q].load(x + (size_t)src * pitch + p.F + c);
+          const T* from = x + (size_t)src * pitch + c;
+#pragma unroll
+          for (int h = 0; h < kRaw; ++h) {
+            v[q][h].load(from + 8 * h);
+            if (kSilu) w[q][h].load(from + p.F + 8 * h);
+          }
         }
       }
     }
 #pragma unroll
-    for (int q = 0; q < kQPieces; ++q) {
+    for (int q = 0; q < kPieces; ++q) {
       uint32_t top = 0;
       if (live[q]) {
-        if (kSilu) {
-          float g[8], u[8], a[8];
-          v[q].get(g);
-          w[q].get(u);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (!silu_mul_fast<T>(g[k], u[k], &a[k])) a[k] = silu_mul_exact<T>(g[k], u[k]);
-          v[q].set(a);
+        for (int h = 0; h < kRaw; ++h) {
+          if (kSilu) {
+            float g[8], u[8], a[8];
+            v[q][h].get(g);
+            w[q][h].get(u);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (!silu_mul_fast<T>(g[k], u[k], &a[k])) a[k] = silu_mul_exact<T>(g[k], u[k]);
+            v[q][h].set(a);
+          }
+          top = max(top, Top<T>::of(v[q][h]));
         }
-        top = Top<T>::of(v[q]);
       }
-      // the four threads of a block are neighbours and live or dead together
+      // the threads of a block are neighbours and live or dead together
       __syncwarp();
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+      for (int o = 1; o < 32 / kVals; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       if (live[q]) {
         const uint32_t bits = Top<T>::as_f32(top);
         const bool finite = bits < 0x7f800000u;
@@ -173,18 +192,26 @@ mx_quant_kernel(const __grid_constant__ MxQuantParams p, const Divisor by_cols, 
         const uint32_t scale = finite ? (ex > 2u ? ex - 2u : 0u) : 255u;
         // 2^-(scale - 127): a normal number for every scale a finite block has
         const float inv = finite ? __uint_as_float((254u - scale) << 23) : 0.0f;
-        float f[8];
-        v[q].get(f);
+        uint32_t codes[kRaw];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) f[k] *= inv;
-        uint32_t codes = pack_e2m1(f);
-        if (!finite) {
-          codes = 0;
-          bad_val = true;
+        for (int h = 0; h < kRaw; ++h) {
+          float f[8];
+          v[q][h].get(f);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] *= inv;
+          codes[h] = pack_e2m1(f);
+          if (!finite) codes[h] = 0;
         }
-        *reinterpret_cast<uint32_t*>(p.codes + (at[q] >> 1)) = codes;
-        if ((lane & 3) == 0) p.scales[at[q] >> 5] = (uint8_t)scale;
-        if (p.rows_out != nullptr) v[q].store(reinterpret_cast<T*>(p.rows_out) + at[q]);
+        bad_val |= !finite;
+        uint8_t* to = p.codes + (at[q] >> 1);
+        if (kRaw == 2) *reinterpret_cast<uint2*>(to) = make_uint2(codes[0], codes[kRaw - 1]);
+        else *reinterpret_cast<uint32_t*>(to) = codes[0];
+        if ((lane & (32 / kVals - 1)) == 0) p.scales[at[q] >> 5] = (uint8_t)scale;
+        if (p.rows_out != nullptr) {
+#pragma unroll
+          for (int h = 0; h < kRaw; ++h)
+            v[q][h].store(reinterpret_cast<T*>(p.rows_out) + at[q] + 8 * h);
+        }
       }
     }
   }
@@ -241,12 +268,15 @@ int grid_for(long long n, int per_block) {
 
 template <typename T>
 cudaError_t quant_typed(const MxQuantParams& p, int act, cudaStream_t stream) {
-  const Divisor by_cols((uint32_t)p.F >> 3);
+  constexpr int kVals = Piece<T>::kVals;
+  const Divisor by_cols((uint32_t)p.F / kVals);
   const int most = (int)(0x7fffffffu / by_cols.d);   // rows of one launch
   for (long long first = 0; first < p.rows; first += most) {
     const long long rows = p.rows - first < most ? p.rows - first : most;
-    const int grid = grid_for(rows * by_cols.d, kQThreads * kQPieces);
-    if (act == LORA_ACT_SILU_MUL)
+    const bool silu = act == LORA_ACT_SILU_MUL;
+    const int grid = grid_for(rows * by_cols.d, kQThreads * (silu ? Piece<T>::template count<true>()
+                                                                  : Piece<T>::template count<false>()));
+    if (silu)
       mx_quant_kernel<T, true><<<grid, kQThreads, 0, stream>>>(p, by_cols, (int)first);
     else
       mx_quant_kernel<T, false><<<grid, kQThreads, 0, stream>>>(p, by_cols, (int)first);
