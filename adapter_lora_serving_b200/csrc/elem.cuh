@@ -36,11 +36,26 @@ template <typename T>
 LORA_DEV uint32_t pack2_any(T t, float lo, float hi) { return pack2(t, lo, hi); }
 LORA_DEV uint32_t pack2_any(float, float lo, float) { return __float_as_uint(lo); }
 
+// 16 bytes, or zeros where `valid` is false: one predicated load without a branch,
+// so that several stay in flight.
+LORA_DEV uint4 load16_if(const void* p, bool valid) {
+  uint4 v;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"(valid ? 1 : 0));
+  return v;
+}
+
 // Eight consecutive elements as raw words (16-byte accesses; two for fp32).
 template <typename T>
 struct Raw8 {
   uint4 v;
   LORA_DEV void load(const T* p) { v = *reinterpret_cast<const uint4*>(p); }
+  LORA_DEV void load_if(const T* p, bool valid) { v = load16_if(p, valid); }
   LORA_DEV void store(T* p) const { *reinterpret_cast<uint4*>(p) = v; }
   LORA_DEV void get(float (&f)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -62,6 +77,11 @@ struct Raw8<float> {
   LORA_DEV void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
+  }
+  LORA_DEV void load_if(const float* p, bool valid) {
+    const uint4 u = load16_if(p, valid), w = load16_if(p + 4, valid);
+    a = make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
+    b = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
   }
   LORA_DEV void store(float* p) const {
     reinterpret_cast<float4*>(p)[0] = a;
