@@ -43,7 +43,6 @@ constexpr int kK = 256;               // elements of k per stage of element tile
 constexpr int kATile = kM * kK / 2;   // 16 KB
 constexpr int kBlockK = 512;          // elements of k per block of scales (16 bytes a row)
 constexpr int kSfAtom = 512;          // scales of 128 rows x 128 elements
-constexpr int kSfSlots = 3;           // blocks of scales in flight
 constexpr int kTurn = 1024;            // an epilogue warp's 16 rows x 32 features of 16 bits
 constexpr int kHeader = 6144;         // barriers, scan scratch and the experts' tile prefix (1025 ints)
 
@@ -51,7 +50,8 @@ template <int BN>
 struct Cfg {
   static constexpr int kBTile = BN * kK / 2;
   static constexpr int kStage = kATile + kBTile;
-  static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : BN >= 64 ? 8 : 9;
+  static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : BN >= 64 ? 8 : BN >= 32 ? 9 : 10;
+  static constexpr int kSfSlots = BN >= 256 ? 3 : BN >= 64 ? 5 : 6;   // blocks of scales in flight
   static constexpr int kAtoms = BN > 128 ? 2 : 1;             // of x, per 128 elements of k
   static constexpr int kSfX = 4 * kAtoms * kSfAtom;
   static constexpr int kSfSlot = 4 * kSfAtom + kSfX;
@@ -67,13 +67,15 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
+enum ScaleCopy { kByTma = 0, kBy8 = 8, kBy4 = 4, kBy1 = 1 };
+
 struct Params {
   MxLinearParams q;
   int ftiles;       // feature tiles of a weight
   int splits;       // CTAs per tile (the cluster size)
   int blocks;       // 512-element blocks of the whole k
   int per_split;    // blocks of a CTA's part
-  int tma_scales;   // scales come by tensor TMA (their rows are multiples of 16 bytes)
+  int scale_copy;   // how scales come: kByTma, or asynchronous copies of 8 or 4 bytes, or bytes
 };
 
 LORA_DEV uint32_t up1024(uint32_t v) { return (v + 1023u) & ~1023u; }
@@ -189,77 +191,25 @@ LORA_DEV Tile tile_of(const Params& p, const Plan& plan, int u) {
   return t;
 }
 
-// The 16 scale bytes of a row's block from byte `at` on, zero past its end.
-LORA_DEV uint4 load_scales(const uint8_t* base, long long row, long long rows, int per_row, int at) {
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-  if (row < rows) {
-    const uint8_t* s = base + row * per_row + at;
-    const int n = min(16, per_row - at);
-    if ((per_row & 7) == 0) {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(s));
-      w[0] = u.x;
-      w[1] = u.y;
-      if (n > 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(s) + 1);
-        w[2] = v.x;
-        w[3] = v.y;
-      }
-    } else if ((per_row & 3) == 0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (4 * i < n) w[i] = __ldg(reinterpret_cast<const uint32_t*>(s) + i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) w[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
-    }
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Scales of a tile's ROWS rows into the order the tensor core reads, block after
+// Scales of a tile into the order the tensor core reads, in place, block after
 // block (the whole warp): lane l has rows l, l + 32, l + 64, l + 96 of an atom; word
-// c of row 32 j + l becomes word j of lane l of atom c.  Raw rows are in the slot
-// already (by TMA, in place), or are loaded here, a block ahead.
-template <int ATOMS, int ROWS, typename RowOf>
-LORA_DEV void order_scales(const Params& p, uint8_t* ring, int slot_bytes, uint64_t* raw,
-                           uint64_t* ready, uint64_t* empty, volatile int* stop, int total,
-                           RowOf row_of, const uint8_t* src, long long nrows, int k0, int blocks) {
+// c of row 32 j + l becomes word j of lane l of atom c.  (Rows past the tile's are
+// whatever the slot held: their products are not stored.)
+template <int ATOMS, int SLOTS>
+LORA_DEV void order_scales(uint8_t* ring, int slot_bytes, uint64_t* raw, uint64_t* ready,
+                           volatile int* stop, uint32_t* flags, int total) {
   const int lane = threadIdx.x & 31;
-  uint4 v[ATOMS][4];
   Ring b;
-  int unit = 0, block = 0;
-  long long row = 0;
-  auto load = [&]() {
-    if (block == 0) row = (long long)row_of(unit) + lane;
+  for (int n = 0; n < total; ++n) {
+    uint8_t* slot = ring + b.s * slot_bytes + lane * 16;
+    if (!wait_or_stop(&raw[b.s], b.round, stop, flags)) break;
+    uint4 v[ATOMS][4];
 #pragma unroll
     for (int h = 0; h < ATOMS; ++h)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        v[h][j] = h * 128 + j * 32 < ROWS
-                      ? load_scales(src, row + h * 128 + j * 32, nrows, p.q.K / 32,
-                                    (k0 + block * kBlockK) / 32)
-                      : make_uint4(0u, 0u, 0u, 0u);
-    if (++block == blocks) {
-      block = 0;
-      ++unit;
-    }
-  };
-  const bool by_tma = p.tma_scales;
-  if (!by_tma && total > 0) load();
-  for (int n = 0; n < total; ++n) {
-    uint8_t* slot = ring + b.s * slot_bytes + lane * 16;
-    if (by_tma) {
-      if (!wait_or_stop(&raw[b.s], b.round, stop, p.q.flags)) break;
-#pragma unroll
-      for (int h = 0; h < ATOMS; ++h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[h][j] = *reinterpret_cast<const uint4*>(slot + (h * 128 + j * 32) * 16);
-      __syncwarp();
-    } else {
-      if (!wait_or_stop(&empty[b.s], b.round ^ 1u, stop, p.q.flags)) break;
-    }
+        v[h][j] = *reinterpret_cast<const uint4*>(slot + (h * 128 + j * 32) * 16);
+    __syncwarp();
 #pragma unroll
     for (int h = 0; h < ATOMS; ++h) {
       uint8_t* dst = slot + h * kSfAtom;
@@ -274,9 +224,43 @@ LORA_DEV void order_scales(const Params& p, uint8_t* ring, int slot_bytes, uint6
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&ready[b.s]);
-    b.next<kSfSlots>();
-    if (!by_tma && n + 1 < total) load();
+    b.next<SLOTS>();
   }
+}
+
+// ROWS rows' 16 scale bytes from byte `at` of row row0 on into a slot (the whole
+// warp), zeros past a row's end and past the last row: copies of N bytes that land
+// later (arriving on `raw`, 32 arrivals), for row pitches that are multiples of N.
+template <int N, int ROWS>
+LORA_DEV void copy_scale_rows(uint8_t* slot, const uint8_t* src, long long row0, long long nrows,
+                              int per_row, int at, uint64_t* raw) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int i = lane; i < ROWS * (16 / N); i += 32) {
+    const int r = i / (16 / N), o = i % (16 / N) * N;
+    const bool valid = row0 + r < nrows && at + o < per_row;
+    const uint8_t* from = valid ? src + (row0 + r) * per_row + at + o : src;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(slot + r * 16 + o)),
+                 "l"(from), "n"(N), "r"(valid ? N : 0)
+                 : "memory");
+  }
+  cp_async_arrive_noinc(raw);
+}
+// Any pitch: byte by byte, through registers.
+template <int ROWS>
+LORA_DEV void copy_scale_bytes(uint8_t* slot, const uint8_t* src, long long row0, long long nrows,
+                               int per_row, int at, uint64_t* raw) {
+  const int lane = threadIdx.x & 31;
+  for (int r = lane; r < ROWS; r += 32) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    const uint8_t* s = src + (row0 + r) * per_row + at;
+    const int n = row0 + r < nrows ? min(16, per_row - at) : 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) w[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
+    *reinterpret_cast<uint4*>(slot + r * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  mbar_arrive(raw);
 }
 
 // 16 lanes x 32 columns of fp32 from tensor memory in the layout of a matrix
@@ -352,9 +336,9 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   uint64_t* empty = full + kS;
   uint64_t* sf_raw = empty + kS;                // a block of scales has landed (by TMA):
                                                 // the weight's, then x's
-  uint64_t* sf_full = sf_raw + 2 * kSfSlots;    // ... is in order
-  uint64_t* sf_empty = sf_full + kSfSlots;  // ... is in tensor memory
-  uint64_t* accfull = sf_empty + kSfSlots;
+  uint64_t* sf_full = sf_raw + 2 * C::kSfSlots;    // ... is in order
+  uint64_t* sf_empty = sf_full + C::kSfSlots;  // ... is in tensor memory
+  uint64_t* accfull = sf_empty + C::kSfSlots;
   uint64_t* accempty = accfull + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 512);
   volatile int* stop = reinterpret_cast<volatile int*>(base + 516);
@@ -362,7 +346,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   int* prefix = reinterpret_cast<int*>(base + 1024);   // up to 1025 ints
   uint8_t* ring = base + kHeader;
   uint8_t* sf_ring = ring + kS * C::kStage;
-  uint8_t* turn = sf_ring + kSfSlots * C::kSfSlot;
+  uint8_t* turn = sf_ring + C::kSfSlots * C::kSfSlot;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = p.splits;
@@ -380,9 +364,10 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kSfSlots; ++i) {
-      mbar_init(&sf_raw[i], 1);
-      mbar_init(&sf_raw[kSfSlots + i], 1);
+    for (int i = 0; i < C::kSfSlots; ++i) {
+      // by TMA one arrival, else one of each copying lane
+      mbar_init(&sf_raw[i], p.scale_copy == kByTma ? 1 : 32);
+      mbar_init(&sf_raw[C::kSfSlots + i], p.scale_copy == kByTma ? 1 : 32);
       mbar_init(&sf_full[i], 2);    // the two scale warps
       mbar_init(&sf_empty[i], 1);
     }
@@ -475,7 +460,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
                             lo + (4 + C::kAtoms * c + h) * (kSfAtom >> 4));
             }
             mma_commit(&sf_empty[b.s]);
-            b.next<kSfSlots>();
+            b.next<C::kSfSlots>();
           }
           if (!(ok = wait_or_stop(&full[r.s], r.round, stop, p.q.flags))) break;
           tc_fence_after();
@@ -501,32 +486,47 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     // 3 those of x.  Lane l has rows l, l + 32, l + 64, l + 96 of an atom; a row's
     // 16 bytes are one word for each of four atoms. ----
     if (warp == 2)
-      order_scales<1, kM>(p, sf_ring, C::kSfSlot, sf_raw, sf_full, sf_empty, stop, units * blocks,
-                          [&](int i) { return tile_of<BN>(p, plan, first_unit + i * unit_step).wrow; },
-                          p.q.w_scales, (long long)p.q.experts * p.q.N, k0, blocks);
+      order_scales<1, C::kSfSlots>(sf_ring, C::kSfSlot, sf_raw, sf_full, stop, p.q.flags,
+                                   units * blocks);
     else
-      order_scales<C::kAtoms, BN>(p, sf_ring + 4 * kSfAtom, C::kSfSlot, sf_raw + kSfSlots, sf_full,
-                                  sf_empty, stop, units * blocks,
-                                  [&](int i) { return tile_of<BN>(p, plan, first_unit + i * unit_step).row0; },
-                                  p.q.x_scales, p.q.rows, k0, blocks);
+      order_scales<C::kAtoms, C::kSfSlots>(sf_ring + 4 * kSfAtom, C::kSfSlot, sf_raw + C::kSfSlots,
+                                           sf_full, stop, p.q.flags, units * blocks);
   } else if (warp == 4 + C::kEpiWarps) {
-    // ---- raw scales, where they come by TMA ----
-    if (p.tma_scales && elect_one()) {
+    // ---- raw scales ----
+    const bool by_tma = p.scale_copy == kByTma;
+    const int per_row = p.q.K / 32;
+    const long long w_rows = (long long)p.q.experts * p.q.N;
+    if (!by_tma || elect_one()) {
       Ring b;
       bool ok = true;
       for (int i = 0; i < units && ok; ++i) {
         const Tile t = tile_of<BN>(p, plan, first_unit + i * unit_step);
         for (int k = 0; k < blocks; ++k) {
           if (!(ok = wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags))) break;
-          uint8_t* slot = sf_ring + b.s * C::kSfSlot;
+          uint8_t* w = sf_ring + b.s * C::kSfSlot;
+          uint8_t* x = w + 4 * kSfAtom;
+          uint64_t *raw_w = &sf_raw[b.s], *raw_x = &sf_raw[C::kSfSlots + b.s];
           const int at = k0 / 32 + k * (kBlockK / 32);
-          mbar_arrive_expect_tx(&sf_raw[b.s], kM * 16);
-          tma_load_2d(slot, &map_ws, at, t.wrow, &sf_raw[b.s]);
-          mbar_arrive_expect_tx(&sf_raw[kSfSlots + b.s], BN * 16);
-          tma_load_2d(slot + 4 * kSfAtom, &map_xs, at, t.row0, &sf_raw[kSfSlots + b.s]);
-          b.next<kSfSlots>();
+          if (by_tma) {
+            mbar_arrive_expect_tx(raw_w, kM * 16);
+            tma_load_2d(w, &map_ws, at, t.wrow, raw_w);
+            mbar_arrive_expect_tx(raw_x, BN * 16);
+            tma_load_2d(x, &map_xs, at, t.row0, raw_x);
+          } else if (p.scale_copy == kBy8) {
+            copy_scale_rows<8, kM>(w, p.q.w_scales, t.wrow, w_rows, per_row, at, raw_w);
+            copy_scale_rows<8, BN>(x, p.q.x_scales, t.row0, p.q.rows, per_row, at, raw_x);
+          } else if (p.scale_copy == kBy4) {
+            copy_scale_rows<4, kM>(w, p.q.w_scales, t.wrow, w_rows, per_row, at, raw_w);
+            copy_scale_rows<4, BN>(x, p.q.x_scales, t.row0, p.q.rows, per_row, at, raw_x);
+          } else {
+            copy_scale_bytes<kM>(w, p.q.w_scales, t.wrow, w_rows, per_row, at, raw_w);
+            copy_scale_bytes<BN>(x, p.q.x_scales, t.row0, p.q.rows, per_row, at, raw_x);
+          }
+          b.next<C::kSfSlots>();
         }
       }
+      // copies of a warp that gave up land before it leaves
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
     // ---- epilogue: lane = feature, column = row of x ----
@@ -542,6 +542,22 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
       const int f = t.f0 + quarter * 32 + lane;
       const bool f_ok = f < p.q.N;
       const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc.s * BN + c_first);
+      if (splits > 1) {
+        // partial sums to shared memory, [column][feature]: the ring is idle, this
+        // being the CTA's only tile and its MMAs done
+        float* part_sums = reinterpret_cast<float*>(ring) + (size_t)c_first * kM + quarter * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < C::kWarpCols / 32; ++c)
+          if (c_first + c * 32 < t.rows) {   // warp-uniform
+            float v[32];
+            tmem_ld_32x32(src + c * 32, v);
+#pragma unroll
+            for (int n = 0; n < 32; ++n)
+              if (c_first + c * 32 + n < BN) part_sums[(c * 32 + n) * kM] = v[n];
+          }
+        tc_fence_before();
+        break;
+      }
       if (sizeof(OT) == 2) {
         // all of it into registers first, so that the accumulator is free early
         uint32_t lo[C::kWarpCols / 32][8], hi[C::kWarpCols / 32][8];
@@ -585,6 +601,33 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   }
 
   __syncwarp();
+  if (splits > 1) {
+    // Sum over the cluster in rank order; each CTA finishes its share of the rows.
+    // Every CTA of the cluster has the same tile, so all of them are here.
+    cluster_sync();
+    if (units > 0) {
+      const Tile t = tile_of<BN>(p, plan, first_unit);
+      const int share = (t.rows + splits - 1) / splits;
+      const int c1 = min(t.rows, (part + 1) * share);
+      const int f = lane * 4;
+      for (int c = part * share + warp; c < c1; c += C::kThreads / 32) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < splits; ++s) {
+          const float4 v = dsmem_ld_f32x4(dsmem_addr(ring + (c * kM + f) * 4, (uint32_t)s));
+          sum.x += v.x; sum.y += v.y; sum.z += v.z; sum.w += v.w;
+        }
+        if (t.f0 + f < p.q.N) {   // N is a multiple of 8
+          OT* o = reinterpret_cast<OT*>(p.q.y) + (size_t)(t.row0 + c) * p.q.N + t.f0 + f;
+          if (sizeof(OT) == 2)
+            *reinterpret_cast<uint2*>(o) =
+                make_uint2(pack2_any(OT(), sum.x, sum.y), pack2_any(OT(), sum.z, sum.w));
+          else
+            *reinterpret_cast<float4*>(o) = sum;
+        }
+      }
+    }
+    cluster_sync();   // no CTA leaves while its sums are read
+  }
   if (*stop) {
     // given up: let copies and MMAs that are still under way land first
     const uint64_t t0 = global_timer_ns();
@@ -656,8 +699,15 @@ cudaError_t dev_sms(int* dev, int* sms) {
   return cudaSuccess;
 }
 
+// Tiles there can be: every expert's last one may be partial.
+long long tile_bound(const MxLinearParams& q, int BN) {
+  const long long ftiles = (q.N + kM - 1) / kM;
+  if (q.expert_offsets == nullptr) return ((long long)q.rows + BN - 1) / BN * ftiles;
+  return ((long long)q.rows / BN + min(q.experts, q.rows)) * ftiles;
+}
+
 template <int BN, typename OT>
-cudaError_t launch(const MxLinearParams& q, cudaStream_t stream, const char** why) {
+cudaError_t launch(const MxLinearParams& q, int splits, cudaStream_t stream, const char** why) {
   typedef Cfg<BN> C;
   int dev = 0, sms = 0;
   cudaError_t err = dev_sms(&dev, &sms);
@@ -682,33 +732,114 @@ cudaError_t launch(const MxLinearParams& q, cudaStream_t stream, const char** wh
   Params p = {};
   p.q = q;
   p.ftiles = (q.N + kM - 1) / kM;
-  p.splits = 1;
   p.blocks = (q.K + kBlockK - 1) / kBlockK;
-  p.per_split = p.blocks;
-  p.tma_scales = q.K % kBlockK == 0;
-  if (p.tma_scales) {
+  p.per_split = (p.blocks + splits - 1) / splits;
+  p.splits = (p.blocks + p.per_split - 1) / p.per_split;   // every CTA has a part
+  p.scale_copy = q.K % kBlockK == 0 ? kByTma : q.K % 256 == 0 ? kBy8 : q.K % 128 == 0 ? kBy4 : kBy1;
+  if (p.scale_copy == kByTma) {
     err = make_map(&map_ws, q.w_scales, (uint64_t)q.K / 32, w_rows, kBlockK / 32, kM, why);
     if (err != cudaSuccess) return err;
     err = make_map(&map_xs, q.x_scales, (uint64_t)q.K / 32, x_rows, kBlockK / 32, BN, why);
     if (err != cudaSuccess) return err;
   }
-  // tiles there can be: every expert's last one may be partial
-  const long long bound =
-      ((long long)(q.rows + BN - 1) / BN + (experts > 1 ? min(experts, q.rows) : 0)) * p.ftiles;
-  const int grid = (int)min((long long)sms, bound);
-  mx_linear_kernel<BN, OT><<<grid, C::kThreads, C::kSmem, stream>>>(map_w, map_x, map_ws, map_xs, p);
-  return cudaGetLastError();
+  const long long tiles = tile_bound(q, BN);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attrs[1];
+  // a cluster for each tile, or one CTA per SM over all tiles
+  cfg.gridDim = dim3((unsigned)(p.splits > 1 ? tiles * p.splits : min((long long)sms, tiles)), 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = (unsigned)p.splits;
+  attrs[0].val.clusterDim.y = 1;
+  attrs[0].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, mx_linear_kernel<BN, OT>, map_w, map_x, map_ws, map_xs, p);
+}
+
+// Clusters of `size` CTAs (one to an SM) that run at once: fewer than SMs / size,
+// for a cluster stays within a group of SMs (45 of three on 148 SMs).
+int clusters_at_once(int dev, int size) {
+  static int known[64][9];
+  std::lock_guard<std::mutex> lk(g_mu);
+  int& n = known[dev][size];
+  if (n == 0) {
+    typedef Cfg<128> C;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)size, 1, 1);
+    cfg.blockDim = dim3(C::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = C::kSmem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int got = 0;
+    if (cudaFuncSetAttribute(mx_linear_kernel<128, __nv_bfloat16>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&got, mx_linear_kernel<128, __nv_bfloat16>, &cfg) != cudaSuccess)
+      got = 0;
+    n = got > 0 ? got : -1;
+  }
+  return n;
+}
+
+// Which tile, and how many CTAs to a tile.  The smallest row tile that holds the
+// rows an expert has on average; and where the tiles do not fill the SMs, as many
+// CTAs to each as do (a cluster of at most eight, each with at least one block of k).
+// With one weight and more than 128 rows both larger tiles are weighed by what a CTA
+// then has to do: a stage costs what its bytes take at 60 a cycle, and a tile an
+// epilogue (cycles, fitted to 8192 and 2048 rows of 4096 by 28672 and 6144).
+struct Shape {
+  int rows, splits;
+};
+Shape choose(const MxLinearParams& q, int dev, int sms) {
+  const int experts = q.expert_offsets != nullptr ? min(q.experts, q.rows) : 1;
+  const long long mean = ((long long)q.rows + experts - 1) / experts;
+  const int blocks = (q.K + kBlockK - 1) / kBlockK;
+  auto splits_for = [&](long long tiles) {
+    // as many as let every tile's cluster run at once
+    int s = (int)min((long long)sms / (tiles > 0 ? tiles : 1), (long long)min(8, blocks));
+    while (s > 1 && clusters_at_once(dev, s) < tiles) --s;
+    return max(1, s);
+  };
+  Shape best = {mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128, 1};
+  best.splits = splits_for(tile_bound(q, best.rows));
+  if (mean <= 128) return best;
+  if (q.expert_offsets != nullptr) return {256, splits_for(tile_bound(q, 256))};
+  double least = 0;
+  for (int bn = 128; bn <= 256; bn += 128) {
+    const long long tiles = tile_bound(q, bn);
+    const int splits = splits_for(tiles);
+    const long long rounds = splits > 1 ? 1 : (tiles + sms - 1) / sms;
+    const double stages = 2.0 * ((blocks + splits - 1) / splits);
+    const double cost = rounds * (stages * (kATile + bn * kK / 2) / 60.0 + 8.0 * bn) +
+                        (splits > 1 ? 1500.0 + 10.0 * bn : 0.0);
+    if (bn == 128 || cost < least) {
+      least = cost;
+      best = {bn, splits};
+    }
+  }
+  return best;
 }
 
 template <typename OT>
 cudaError_t launch_typed(const MxLinearParams& q, cudaStream_t stream, const char** why) {
-  const int experts = q.expert_offsets != nullptr ? q.experts : 1;
-  const long long mean = ((long long)q.rows + experts - 1) / experts;
-  if (mean <= 16) return launch<16, OT>(q, stream, why);
-  if (mean <= 32) return launch<32, OT>(q, stream, why);
-  if (mean <= 64) return launch<64, OT>(q, stream, why);
-  if (mean <= 128) return launch<128, OT>(q, stream, why);
-  return launch<256, OT>(q, stream, why);
+  int dev = 0, sms = 0;
+  const cudaError_t err = dev_sms(&dev, &sms);
+  if (err != cudaSuccess) return err;
+  const Shape s = choose(q, dev, sms);
+  switch (s.rows) {
+    case 16: return launch<16, OT>(q, s.splits, stream, why);
+    case 32: return launch<32, OT>(q, s.splits, stream, why);
+    case 64: return launch<64, OT>(q, s.splits, stream, why);
+    case 128: return launch<128, OT>(q, s.splits, stream, why);
+    default: return launch<256, OT>(q, s.splits, stream, why);
+  }
 }
 
 }  // namespace

@@ -435,7 +435,8 @@ def test_linear_one_tile():
 
 
 @pytest.mark.parametrize("rows", [1, 7, 16, 17, 33, 64, 65, 128, 129, 300])
-@pytest.mark.parametrize("K,N", [(256, 128), (32, 8), (96, 136), (1056, 264), (2048, 512)])
+@pytest.mark.parametrize("K,N", [(256, 128), (32, 8), (96, 136), (1056, 264), (2048, 512), (640, 392),
+                                 (768, 2048), (4608, 1000)])
 def test_linear(rows, K, N):
     _check_linear("bf16", rows, K, N)
 
@@ -491,7 +492,7 @@ def _check_expert(name, counts, K, N, seed=0, offsets=None, tail=0, start=0):
 
 @pytest.mark.parametrize("counts", [[1], [0, 0, 5, 0], [3, 1, 0, 17, 2, 2], [40, 0, 64, 1],
                                     [130, 257, 0, 12, 128], [1] * 40, [0, 0, 0]])
-@pytest.mark.parametrize("K,N", [(256, 128), (96, 72), (800, 328)])
+@pytest.mark.parametrize("K,N", [(256, 128), (96, 72), (800, 328), (768, 512), (2048, 136), (384, 3000)])
 def test_expert_linear(counts, K, N):
     _check_expert("bf16", counts, K, N)
 
