@@ -50,7 +50,7 @@ template <int BN>
 struct Cfg {
   static constexpr int kBTile = BN * kK / 2;
   static constexpr int kStage = kATile + kBTile;
-  static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : BN >= 64 ? 8 : BN >= 32 ? 9 : 10;
+  static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : BN >= 64 ? 8 : BN >= 32 ? 9 : 8;
   static constexpr int kSfSlots = BN >= 256 ? 3 : BN >= 64 ? 5 : 6;   // blocks of scales in flight
   static constexpr int kAtoms = BN > 128 ? 2 : 1;             // of x, per 128 elements of k
   static constexpr int kSfX = 4 * kAtoms * kSfAtom;
