@@ -80,11 +80,25 @@ struct Params {
 
 LORA_DEV uint32_t up1024(uint32_t v) { return (v + 1023u) & ~1023u; }
 
+// Phase test that acquires at cluster scope (for arrivals of another CTA).
+LORA_DEV bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait that also gives up when another role of the CTA has.  The clock is looked
 // at only now and then.
+template <bool CLUSTER = false>
 LORA_DEV bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, uint32_t* flags) {
   uint64_t t0 = 0;
-  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+  for (uint32_t i = 1; !(CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)); ++i) {
     if (*stop) return false;
     if ((i & 255u) == 0u) {
       const uint64_t t = global_timer_ns();
@@ -97,6 +111,17 @@ LORA_DEV bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, u
     }
   }
   return true;
+}
+
+// The same barrier of the cluster's first CTA, and an arrival there.
+LORA_DEV uint32_t at_first(const uint64_t* bar) { return dsmem_addr(bar, 0); }
+// (Release at the default scope: what the arrivals follow is ordered for the tensor
+// core by a proxy fence or a tcgen05 fence already, and a release at cluster scope
+// made the pair kernel's stages a third longer: 470 us for 8192 x 4096 x 28672, 351
+// without.)
+LORA_DEV void arrive_at_first(const uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at_first(bar))
+               : "memory");
 }
 // A ring position and the parity of its current round.
 struct Ring {
@@ -172,7 +197,34 @@ struct Plan {
   int tiles;
 };
 
-template <int BN>
+// Tiles of BN rows before each expert (the whole CTA; __syncthreads follows).
+template <int BN, int THREADS>
+LORA_DEV Plan make_plan(const Params& p, int* prefix, int* scratch) {
+  Plan plan = {prefix, p.q.expert_offsets, 0};
+  if (plan.offsets == nullptr) {
+    plan.tiles = ((p.q.rows + BN - 1) / BN) * p.ftiles;
+    return plan;
+  }
+  uint32_t bad = 0;
+  if (threadIdx.x == 0) prefix[0] = 0;
+  for (int e0 = 0; e0 < p.q.experts; e0 += THREADS) {
+    const int e = e0 + (int)threadIdx.x;
+    int cnt = 0;
+    if (e < p.q.experts) {
+      const int lo = plan.offsets[e], hi = plan.offsets[e + 1];
+      if (lo < 0 || hi > p.q.rows || hi < lo) bad |= LORA_FLAG_BAD_OFFSETS;
+      else cnt = (hi - lo + BN - 1) / BN * p.ftiles;
+    }
+    int tot;
+    const int inc = block_inclusive_scan<THREADS>(cnt, scratch, &tot);
+    if (e < p.q.experts) prefix[e + 1] = plan.tiles + inc;
+    plan.tiles += tot;
+  }
+  if (blockIdx.x == 0) raise_flag(p.q.flags, bad);
+  return plan;
+}
+
+template <int BN, int FEATURES = kM>
 LORA_DEV Tile tile_of(const Params& p, const Plan& plan, int u) {
   Tile t;
   int e = 0, lo = 0, hi = p.q.rows;
@@ -186,7 +238,7 @@ LORA_DEV Tile tile_of(const Params& p, const Plan& plan, int u) {
   const int f = u / rt;
   t.row0 = lo + (u - f * rt) * BN;
   t.rows = min(BN, hi - t.row0);
-  t.f0 = f * kM;
+  t.f0 = f * FEATURES;
   t.wrow = e * p.q.N + t.f0;
   return t;
 }
@@ -195,7 +247,7 @@ LORA_DEV Tile tile_of(const Params& p, const Plan& plan, int u) {
 // block (the whole warp): lane l has rows l, l + 32, l + 64, l + 96 of an atom; word
 // c of row 32 j + l becomes word j of lane l of atom c.  (Rows past the tile's are
 // whatever the slot held: their products are not stored.)
-template <int ATOMS, int SLOTS>
+template <int ATOMS, int SLOTS, bool PAIR = false>
 LORA_DEV void order_scales(uint8_t* ring, int slot_bytes, uint64_t* raw, uint64_t* ready,
                            volatile int* stop, uint32_t* flags, int total) {
   const int lane = threadIdx.x & 31;
@@ -223,7 +275,10 @@ LORA_DEV void order_scales(uint8_t* ring, int slot_bytes, uint64_t* raw, uint64_
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&ready[b.s]);
+    if (lane == 0) {
+      if (PAIR) arrive_at_first(&ready[b.s]);
+      else mbar_arrive(&ready[b.s]);
+    }
     b.next<SLOTS>();
   }
 }
@@ -384,31 +439,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     tmem_alloc(tmem_slot, C::kCols);
     tmem_relinquish();
   }
-  Plan plan;
-  plan.prefix = prefix;
-  plan.offsets = p.q.expert_offsets;
-  if (plan.offsets == nullptr) {
-    plan.tiles = ((p.q.rows + BN - 1) / BN) * p.ftiles;
-  } else {
-    int carry = 0;
-    uint32_t bad = 0;
-    if (threadIdx.x == 0) prefix[0] = 0;
-    for (int e0 = 0; e0 < p.q.experts; e0 += C::kThreads) {
-      const int e = e0 + threadIdx.x;
-      int cnt = 0;
-      if (e < p.q.experts) {
-        const int lo = plan.offsets[e], hi = plan.offsets[e + 1];
-        if (lo < 0 || hi > p.q.rows || hi < lo) bad |= LORA_FLAG_BAD_OFFSETS;
-        else cnt = (hi - lo + BN - 1) / BN * p.ftiles;
-      }
-      int tot;
-      const int inc = block_inclusive_scan<C::kThreads>(cnt, scratch, &tot);
-      if (e < p.q.experts) prefix[e + 1] = carry + inc;
-      carry += tot;
-    }
-    if (blockIdx.x == 0) raise_flag(p.q.flags, bad);
-    plan.tiles = carry;
-  }
+  const Plan plan = make_plan<BN, C::kThreads>(p, prefix, scratch);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -642,6 +673,290 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
   }
 }
 
+// ---------------------------------------------------------------------------
+// Two CTAs on one tile of 256 features x 256 rows (cta_group::2), for products of
+// many rows.  Each CTA holds 128 features of the weight and 128 of the rows, and
+// the tensor cores of both read them from both: 8 KB of shared memory per MMA and
+// SM instead of the 12 that a 128 x 256 tile of one CTA reads, and as much less to
+// fetch, which is what bounds that tile (a stage takes 795 cycles there, 540 being
+// the tensor core's).  Each CTA brings its own element tiles, the scales of its
+// features and those of all rows; the first CTA issues the MMAs and the copies of
+// scales (they run in both), waiting on barriers on which both arrive, and its
+// commits arrive in both.
+// ---------------------------------------------------------------------------
+
+struct PairCfg {
+  static constexpr int kRows = 256;
+  static constexpr int kStage = 2 * kATile;      // 128 features and 128 rows
+  static constexpr int kStages = 6;
+  static constexpr int kSfSlot = 12 * kSfAtom;   // per 512 of k: 4 atoms of W, 8 of X
+  static constexpr int kSfSlots = 3;
+  static constexpr int kEpiWarps = 8;
+  static constexpr int kThreads = 160 + 32 * kEpiWarps;
+  static constexpr int kSmem = 1024 + kHeader + kStages * kStage + kSfSlots * kSfSlot + kEpiWarps * kTurn;
+  static constexpr int kSfCols = 48;             // two sets behind the accumulator's 256 columns
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
+
+constexpr uint32_t mxf4_pair_idesc(uint32_t half) {
+  return ((half * 2u) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(PairCfg::kRows >> 3) << 17) |
+         (1u << 23) | ((uint32_t)(2 * kM >> 7) << 27) | ((half * 2u) << 29);
+}
+LORA_DEV void mma_mxf4_pair(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t sfa,
+                            uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %7};\n\t"
+      "mov.b64 b, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X "
+      "[%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(kDescTile)
+      : "memory");
+}
+LORA_DEV void copy_scales_pair(uint32_t taddr, uint32_t lo) {
+  asm volatile(
+      "{\n\t.reg .b64 d;\n\t"
+      "mov.b64 d, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr),
+      "r"(lo), "r"(kDescScale)
+      : "memory");
+}
+// Arrives on `bar` of both CTAs once what this thread issued so far is done.
+LORA_DEV void commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// A tile into this CTA's memory, counted on a barrier of the pair's first.
+LORA_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+template <typename OT>
+__global__ void __launch_bounds__(PairCfg::kThreads, 1)
+mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ CUtensorMap map_x,
+                      const __grid_constant__ CUtensorMap map_ws,
+                      const __grid_constant__ CUtensorMap map_xs, const Params p) {
+  typedef PairCfg C;
+  constexpr int kS = C::kStages, kSl = C::kSfSlots;
+  extern __shared__ uint8_t mx_smem[];
+  uint8_t* base = mx_smem + (up1024(smem_u32(mx_smem)) - smem_u32(mx_smem));
+  uint64_t* full = reinterpret_cast<uint64_t*>(base);   // (the first CTA's are used)
+  uint64_t* empty = full + kS;
+  uint64_t* sf_raw = empty + kS;
+  uint64_t* sf_full = sf_raw + 2 * kSl;                  // (the first CTA's)
+  uint64_t* sf_empty = sf_full + kSl;
+  uint64_t* accfull = sf_empty + kSl;
+  uint64_t* accempty = accfull + 1;                      // (the first CTA's)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 512);
+  volatile int* stop = reinterpret_cast<volatile int*>(base + 516);
+  int* scratch = reinterpret_cast<int*>(base + 576);
+  int* prefix = reinterpret_cast<int*>(base + 1024);
+  uint8_t* ring = base + kHeader;
+  uint8_t* sf_ring = ring + kS * C::kStage;
+  uint8_t* turn = sf_ring + kSl * C::kSfSlot;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int first_unit = (int)blockIdx.x / 2, unit_step = (int)gridDim.x / 2;
+  const int stages = (p.q.K + kK - 1) / kK, blocks = p.blocks;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kSl; ++i) {
+      mbar_init(&sf_raw[i], 1);
+      mbar_init(&sf_raw[kSl + i], 1);
+      mbar_init(&sf_full[i], 4);                // two scale warps of each CTA
+      mbar_init(&sf_empty[i], 1);
+    }
+    mbar_init(accfull, 1);
+    mbar_init(accempty, 2 * C::kEpiWarps);
+    *stop = 0;
+    fence_mbar_init();
+    prefetch_tensormap(&map_w);
+    prefetch_tensormap(&map_x);
+    prefetch_tensormap(&map_ws);
+    prefetch_tensormap(&map_xs);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(tmem_slot))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  const Plan plan = make_plan<C::kRows, C::kThreads>(p, prefix, scratch);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the barriers of both CTAs are set up
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int units = plan.tiles > first_unit ? (plan.tiles - first_unit - 1) / unit_step + 1 : 0;
+  // this CTA's share of a unit: 128 of its features
+  auto unit = [&](int i) {
+    Tile t = tile_of<C::kRows, 2 * kM>(p, plan, first_unit + i * unit_step);
+    t.f0 += rank * kM;
+    t.wrow += rank * kM;
+    return t;
+  };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      Ring r;
+      for (int i = 0; i < units && !*stop; ++i) {
+        const Tile t = unit(i);
+        for (int k = 0; k < stages; ++k) {
+          if (!wait_or_stop(&empty[r.s], r.round ^ 1u, stop, p.q.flags)) break;
+          uint8_t* slot = ring + r.s * C::kStage;
+          const uint32_t bar = at_first(&full[r.s]);
+          if (rank == 0) mbar_arrive_expect_tx(&full[r.s], 2 * C::kStage);
+          tma_load_2d_pair(slot, &map_w, k * (kK / 2), t.wrow, bar);
+          tma_load_2d_pair(slot + kATile, &map_x, k * (kK / 2), t.row0 + rank * (C::kRows / 2), bar);
+          r.next<kS>();
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && elect_one()) {
+      Ring r, b, acc;
+      const uint32_t ring_lo = desc_lo(smem_u32(ring)), sf_lo = desc_lo(smem_u32(sf_ring));
+      bool ok = true;
+      for (int i = 0; i < units && ok; ++i) {
+        if (!(ok = wait_or_stop<true>(accempty, acc.round ^ 1u, stop, p.q.flags))) break;
+        tc_fence_after();
+        uint32_t sf = 0;
+        for (int k = 0; k < stages; ++k) {
+          if ((k & 1) == 0) {
+            if (!(ok = wait_or_stop<true>(&sf_full[b.s], b.round, stop, p.q.flags))) break;
+            tc_fence_after();
+            sf = tmem + (uint32_t)(C::kRows + (k & 2 ? C::kSfCols : 0));
+            const uint32_t lo = sf_lo + (uint32_t)b.s * (C::kSfSlot >> 4);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              copy_scales_pair(sf + 4 * c, lo + c * (kSfAtom >> 4));
+              copy_scales_pair(sf + 16 + 8 * c, lo + (4 + 2 * c) * (kSfAtom >> 4));
+              copy_scales_pair(sf + 20 + 8 * c, lo + (5 + 2 * c) * (kSfAtom >> 4));
+            }
+            commit_pair(&sf_empty[b.s]);
+            b.next<kSl>();
+          }
+          if (!(ok = wait_or_stop(&full[r.s], r.round, stop, p.q.flags))) break;
+          tc_fence_after();
+          const uint32_t a_lo = ring_lo + (uint32_t)r.s * (C::kStage >> 4);
+          const uint32_t b_lo = a_lo + (kATile >> 4);
+          const uint32_t sfk = sf + (k & 1 ? 8u : 0u), sfx = sf + 16u + (k & 1 ? 16u : 0u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_mxf4_pair(tmem, a_lo + 2 * j, b_lo + 2 * j, mxf4_pair_idesc(j & 1),
+                          sfk + 4 * (j >> 1), sfx + 8 * (j >> 1), (k | j) != 0 ? 1u : 0u);
+          commit_pair(&empty[r.s]);
+          r.next<kS>();
+        }
+        if (!ok) break;
+        commit_pair(accfull);
+        acc.next<1>();
+      }
+    }
+  } else if (warp == 2) {
+    order_scales<1, kSl, true>(sf_ring, C::kSfSlot, sf_raw, sf_full, stop, p.q.flags, units * blocks);
+  } else if (warp == 3) {
+    order_scales<2, kSl, true>(sf_ring + 4 * kSfAtom, C::kSfSlot, sf_raw + kSl, sf_full, stop,
+                               p.q.flags, units * blocks);
+  } else if (warp == 4 + C::kEpiWarps) {
+    if (elect_one()) {
+      Ring b;
+      bool ok = true;
+      for (int i = 0; i < units && ok; ++i) {
+        const Tile t = unit(i);
+        for (int k = 0; k < blocks; ++k) {
+          if (!(ok = wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags))) break;
+          uint8_t* slot = sf_ring + b.s * C::kSfSlot;
+          mbar_arrive_expect_tx(&sf_raw[b.s], kM * 16);
+          tma_load_2d(slot, &map_ws, k * (kBlockK / 32), t.wrow, &sf_raw[b.s]);
+          mbar_arrive_expect_tx(&sf_raw[kSl + b.s], C::kRows * 16);
+          tma_load_2d(slot + 4 * kSfAtom, &map_xs, k * (kBlockK / 32), t.row0, &sf_raw[kSl + b.s]);
+          b.next<kSl>();
+        }
+      }
+    }
+  } else {
+    const int quarter = warp & 3;
+    const int c_first = ((warp - 4) >> 2) * (C::kRows / 2);
+    OT* y = reinterpret_cast<OT*>(p.q.y);
+    uint32_t round = 0;
+    for (int i = 0; i < units; ++i, round ^= 1u) {
+      const Tile t = unit(i);
+      if (!wait_or_stop(accfull, round, stop, p.q.flags)) break;
+      __syncwarp();
+      tc_fence_after();
+      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c_first;
+      const int f = t.f0 + quarter * 32;
+      constexpr int kParts = C::kRows / 2 / 32;
+      if (sizeof(OT) == 2) {
+        uint32_t lo[kParts][8], hi[kParts][8];
+#pragma unroll
+        for (int c = 0; c < kParts; ++c)
+          if (c_first + c * 32 < t.rows) {   // warp-uniform
+            tmem_ld_fragments<OT>(src + c * 32, lo[c]);
+            tmem_ld_fragments<OT>(src + (16u << 16) + c * 32, hi[c]);
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at_first(accempty);
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) {
+          const int c0 = c_first + c * 32;
+          if (c0 < t.rows)
+            store_fragments(y + (size_t)(t.row0 + c0) * p.q.N, p.q.N, f, t.rows - c0,
+                            turn + (warp - 4) * kTurn, lo[c], hi[c]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) {
+          const int c0 = c_first + c * 32;
+          if (c0 < t.rows) {
+            float v[32];
+            tmem_ld_32x32(src + c * 32, v);
+            if (f + lane < p.q.N) {
+              float* o = reinterpret_cast<float*>(p.q.y) + (size_t)(t.row0 + c0) * p.q.N + f + lane;
+#pragma unroll
+              for (int n = 0; n < 32; ++n)
+                if (c0 + n < t.rows) o[(size_t)n * p.q.N] = v[n];
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_at_first(accempty);
+      }
+    }
+  }
+
+  __syncwarp();
+  if (*stop) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) {
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // neither CTA leaves while the other reads its memory or arrives there
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -759,6 +1074,60 @@ cudaError_t launch(const MxLinearParams& q, int splits, cudaStream_t stream, con
   return cudaLaunchKernelEx(&cfg, mx_linear_kernel<BN, OT>, map_w, map_x, map_ws, map_xs, p);
 }
 
+// Tiles of the pair kernel there can be.
+long long pair_bound(const MxLinearParams& q) {
+  const long long ftiles = (q.N + 2 * kM - 1) / (2 * kM);
+  if (q.expert_offsets == nullptr) return ((long long)q.rows + 255) / 256 * ftiles;
+  return ((long long)q.rows / 256 + min(q.experts, q.rows)) * ftiles;
+}
+
+template <typename OT>
+cudaError_t launch_pair(const MxLinearParams& q, int sms, cudaStream_t stream, const char** why) {
+  typedef PairCfg C;
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  static bool attr[64];
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!attr[dev]) {
+      err = cudaFuncSetAttribute(mx_linear_pair_kernel<OT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      if (err != cudaSuccess) return err;
+      attr[dev] = true;
+    }
+  }
+  const uint64_t w_rows = (uint64_t)(q.expert_offsets != nullptr ? q.experts : 1) * q.N;
+  CUtensorMap map_w, map_x, map_ws, map_xs;
+  err = make_map(&map_w, q.w_codes, (uint64_t)q.K / 2, w_rows, kK / 2, kM, why);
+  if (err == cudaSuccess)
+    err = make_map(&map_x, q.x_codes, (uint64_t)q.K / 2, (uint64_t)q.rows, kK / 2, C::kRows / 2, why);
+  if (err == cudaSuccess)
+    err = make_map(&map_ws, q.w_scales, (uint64_t)q.K / 32, w_rows, kBlockK / 32, kM, why);
+  if (err == cudaSuccess)
+    err = make_map(&map_xs, q.x_scales, (uint64_t)q.K / 32, (uint64_t)q.rows, kBlockK / 32, C::kRows, why);
+  if (err != cudaSuccess) return err;
+  Params p = {};
+  p.q = q;
+  p.ftiles = (q.N + 2 * kM - 1) / (2 * kM);
+  p.splits = 1;
+  p.blocks = p.per_split = q.K / kBlockK;
+  p.scale_copy = kByTma;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attrs[1];
+  cfg.gridDim = dim3((unsigned)(2 * min((long long)sms / 2, pair_bound(q))), 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = 2;
+  attrs[0].val.clusterDim.y = 1;
+  attrs[0].val.clusterDim.z = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mx_linear_pair_kernel<OT>, map_w, map_x, map_ws, map_xs, p);
+}
+
 // Clusters of `size` CTAs (one to an SM) that run at once: fewer than SMs / size,
 // for a cluster stays within a group of SMs (45 of three on 148 SMs).
 int clusters_at_once(int dev, int size) {
@@ -833,6 +1202,8 @@ cudaError_t launch_typed(const MxLinearParams& q, cudaStream_t stream, const cha
   const cudaError_t err = dev_sms(&dev, &sms);
   if (err != cudaSuccess) return err;
   const Shape s = choose(q, dev, sms);
+  if (s.rows == 256 && s.splits == 1 && q.K % kBlockK == 0 && pair_bound(q) >= sms / 2)
+    return launch_pair<OT>(q, sms, stream, why);
   switch (s.rows) {
     case 16: return launch<16, OT>(q, s.splits, stream, why);
     case 32: return launch<32, OT>(q, s.splits, stream, why);

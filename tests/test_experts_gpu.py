@@ -453,6 +453,18 @@ def test_linear_many_tiles():
     _check_linear("bf16", 5, 512, 60000)
 
 
+@pytest.mark.parametrize("name,rows,K,N", [("f32", 2304, 512, 2304), ("bf16", 2300, 1024, 2440),
+                                           ("bf16", 4096, 512, 8192), ("f16", 300, 1536, 9736)])
+def test_linear_many_rows(name, rows, K, N):
+    """The tiles that two CTAs share; partial ones at both ends."""
+    _check_linear(name, rows, K, N, spread=0.5)
+
+
+def test_expert_linear_many_rows():
+    for name in ("bf16", "f32"):
+        _check_expert(name, [400, 0, 300, 1, 900], 512, 4000, tail=3)
+
+
 def test_linear_rerun_bit_exact():
     t = _torch()
     rng = np.random.default_rng(9)
