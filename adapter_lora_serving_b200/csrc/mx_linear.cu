@@ -674,8 +674,8 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 }
 
 // ---------------------------------------------------------------------------
-// Two CTAs on one tile of 256 features x 256 rows (cta_group::2), for products of
-// many rows.  Each CTA holds 128 features of the weight and 128 of the rows, and
+// Two CTAs on one tile of 256 features x 256 (or 128) rows (cta_group::2), for
+// products of many rows.  Each CTA holds 128 features of the weight and 128 of the rows, and
 // the tensor cores of both read them from both: 8 KB of shared memory per MMA and
 // SM instead of the 12 that a 128 x 256 tile of one CTA reads, and as much less to
 // fetch, which is what bounds that tile (a stage takes 795 cycles there, 540 being
@@ -685,22 +685,26 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 // commits arrive in both.
 // ---------------------------------------------------------------------------
 
+template <int ROWS>
 struct PairCfg {
-  static constexpr int kRows = 256;
-  static constexpr int kStage = 2 * kATile;      // 128 features and 128 rows
-  static constexpr int kStages = 6;
-  static constexpr int kSfSlot = 12 * kSfAtom;   // per 512 of k: 4 atoms of W, 8 of X
-  static constexpr int kSfSlots = 3;
+  static constexpr int kRows = ROWS;
+  static constexpr int kBTile = ROWS / 2 * kK / 2;
+  static constexpr int kStage = kATile + kBTile;             // 128 features and half of the rows
+  static constexpr int kStages = ROWS == 256 ? 6 : 8;
+  static constexpr int kAtoms = ROWS / 128;
+  static constexpr int kSfSlot = (4 + 4 * kAtoms) * kSfAtom; // per 512 of k: of W, of all of X
+  static constexpr int kSfSlots = ROWS == 256 ? 3 : 4;
   static constexpr int kEpiWarps = 8;
   static constexpr int kThreads = 160 + 32 * kEpiWarps;
   static constexpr int kSmem = 1024 + kHeader + kStages * kStage + kSfSlots * kSfSlot + kEpiWarps * kTurn;
-  static constexpr int kSfCols = 48;             // two sets behind the accumulator's 256 columns
+  static constexpr int kAcc = 256 / ROWS;                    // accumulators: 256 columns in all
+  static constexpr int kSfCols = 16 + 16 * kAtoms;           // two sets behind them
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
-constexpr uint32_t mxf4_pair_idesc(uint32_t half) {
-  return ((half * 2u) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(PairCfg::kRows >> 3) << 17) |
-         (1u << 23) | ((uint32_t)(2 * kM >> 7) << 27) | ((half * 2u) << 29);
+constexpr uint32_t mxf4_pair_idesc(int rows, uint32_t half) {
+  return ((half * 2u) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(rows >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(2 * kM >> 7) << 27) | ((half * 2u) << 29);
 }
 LORA_DEV void mma_mxf4_pair(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t sfa,
                             uint32_t sfb, uint32_t accumulate) {
@@ -739,13 +743,13 @@ LORA_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* map, int c0, int c1
       : "memory");
 }
 
-template <typename OT>
-__global__ void __launch_bounds__(PairCfg::kThreads, 1)
+template <int ROWS, typename OT>
+__global__ void __launch_bounds__(PairCfg<ROWS>::kThreads, 1)
 mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ CUtensorMap map_x,
                       const __grid_constant__ CUtensorMap map_ws,
                       const __grid_constant__ CUtensorMap map_xs, const Params p) {
-  typedef PairCfg C;
+  typedef PairCfg<ROWS> C;
   constexpr int kS = C::kStages, kSl = C::kSfSlots;
   extern __shared__ uint8_t mx_smem[];
   uint8_t* base = mx_smem + (up1024(smem_u32(mx_smem)) - smem_u32(mx_smem));
@@ -755,7 +759,7 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
   uint64_t* sf_full = sf_raw + 2 * kSl;                  // (the first CTA's)
   uint64_t* sf_empty = sf_full + kSl;
   uint64_t* accfull = sf_empty + kSl;
-  uint64_t* accempty = accfull + 1;                      // (the first CTA's)
+  uint64_t* accempty = accfull + C::kAcc;                // (the first CTA's)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + 512);
   volatile int* stop = reinterpret_cast<volatile int*>(base + 516);
   int* scratch = reinterpret_cast<int*>(base + 576);
@@ -780,8 +784,10 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
       mbar_init(&sf_full[i], 4);                // two scale warps of each CTA
       mbar_init(&sf_empty[i], 1);
     }
-    mbar_init(accfull, 1);
-    mbar_init(accempty, 2 * C::kEpiWarps);
+    for (int i = 0; i < C::kAcc; ++i) {
+      mbar_init(&accfull[i], 1);
+      mbar_init(&accempty[i], 2 * C::kEpiWarps);
+    }
     *stop = 0;
     fence_mbar_init();
     prefetch_tensormap(&map_w);
@@ -832,20 +838,23 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
       const uint32_t ring_lo = desc_lo(smem_u32(ring)), sf_lo = desc_lo(smem_u32(sf_ring));
       bool ok = true;
       for (int i = 0; i < units && ok; ++i) {
-        if (!(ok = wait_or_stop<true>(accempty, acc.round ^ 1u, stop, p.q.flags))) break;
+        if (!(ok = wait_or_stop<true>(&accempty[acc.s], acc.round ^ 1u, stop, p.q.flags))) break;
         tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(acc.s * ROWS);
         uint32_t sf = 0;
         for (int k = 0; k < stages; ++k) {
           if ((k & 1) == 0) {
             if (!(ok = wait_or_stop<true>(&sf_full[b.s], b.round, stop, p.q.flags))) break;
             tc_fence_after();
-            sf = tmem + (uint32_t)(C::kRows + (k & 2 ? C::kSfCols : 0));
+            sf = tmem + (uint32_t)(256 + (k & 2 ? C::kSfCols : 0));
             const uint32_t lo = sf_lo + (uint32_t)b.s * (C::kSfSlot >> 4);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               copy_scales_pair(sf + 4 * c, lo + c * (kSfAtom >> 4));
-              copy_scales_pair(sf + 16 + 8 * c, lo + (4 + 2 * c) * (kSfAtom >> 4));
-              copy_scales_pair(sf + 20 + 8 * c, lo + (5 + 2 * c) * (kSfAtom >> 4));
+#pragma unroll
+              for (int h = 0; h < C::kAtoms; ++h)
+                copy_scales_pair(sf + 16 + 4 * (C::kAtoms * c + h),
+                                 lo + (4 + C::kAtoms * c + h) * (kSfAtom >> 4));
             }
             commit_pair(&sf_empty[b.s]);
             b.next<kSl>();
@@ -854,23 +863,23 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
           tc_fence_after();
           const uint32_t a_lo = ring_lo + (uint32_t)r.s * (C::kStage >> 4);
           const uint32_t b_lo = a_lo + (kATile >> 4);
-          const uint32_t sfk = sf + (k & 1 ? 8u : 0u), sfx = sf + 16u + (k & 1 ? 16u : 0u);
+          const uint32_t sfk = sf + (k & 1 ? 8u : 0u), sfx = sf + 16u + (k & 1 ? 8u * C::kAtoms : 0u);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_mxf4_pair(tmem, a_lo + 2 * j, b_lo + 2 * j, mxf4_pair_idesc(j & 1),
-                          sfk + 4 * (j >> 1), sfx + 8 * (j >> 1), (k | j) != 0 ? 1u : 0u);
+            mma_mxf4_pair(d, a_lo + 2 * j, b_lo + 2 * j, mxf4_pair_idesc(ROWS, j & 1),
+                          sfk + 4 * (j >> 1), sfx + 4 * C::kAtoms * (j >> 1), (k | j) != 0 ? 1u : 0u);
           commit_pair(&empty[r.s]);
           r.next<kS>();
         }
         if (!ok) break;
-        commit_pair(accfull);
-        acc.next<1>();
+        commit_pair(&accfull[acc.s]);
+        acc.next<C::kAcc>();
       }
     }
   } else if (warp == 2) {
     order_scales<1, kSl, true>(sf_ring, C::kSfSlot, sf_raw, sf_full, stop, p.q.flags, units * blocks);
   } else if (warp == 3) {
-    order_scales<2, kSl, true>(sf_ring + 4 * kSfAtom, C::kSfSlot, sf_raw + kSl, sf_full, stop,
+    order_scales<C::kAtoms, kSl, true>(sf_ring + 4 * kSfAtom, C::kSfSlot, sf_raw + kSl, sf_full, stop,
                                p.q.flags, units * blocks);
   } else if (warp == 4 + C::kEpiWarps) {
     if (elect_one()) {
@@ -893,13 +902,13 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
     const int quarter = warp & 3;
     const int c_first = ((warp - 4) >> 2) * (C::kRows / 2);
     OT* y = reinterpret_cast<OT*>(p.q.y);
-    uint32_t round = 0;
-    for (int i = 0; i < units; ++i, round ^= 1u) {
+    Ring acc;
+    for (int i = 0; i < units; ++i, acc.next<C::kAcc>()) {
       const Tile t = unit(i);
-      if (!wait_or_stop(accfull, round, stop, p.q.flags)) break;
+      if (!wait_or_stop(&accfull[acc.s], acc.round, stop, p.q.flags)) break;
       __syncwarp();
       tc_fence_after();
-      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)c_first;
+      const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc.s * ROWS + c_first);
       const int f = t.f0 + quarter * 32;
       constexpr int kParts = C::kRows / 2 / 32;
       if (sizeof(OT) == 2) {
@@ -912,7 +921,7 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
           }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at_first(accempty);
+        if (lane == 0) arrive_at_first(&accempty[acc.s]);
 #pragma unroll
         for (int c = 0; c < kParts; ++c) {
           const int c0 = c_first + c * 32;
@@ -937,7 +946,7 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at_first(accempty);
+        if (lane == 0) arrive_at_first(&accempty[acc.s]);
       }
     }
   }
@@ -1075,15 +1084,15 @@ cudaError_t launch(const MxLinearParams& q, int splits, cudaStream_t stream, con
 }
 
 // Tiles of the pair kernel there can be.
-long long pair_bound(const MxLinearParams& q) {
+long long pair_bound(const MxLinearParams& q, int rows) {
   const long long ftiles = (q.N + 2 * kM - 1) / (2 * kM);
-  if (q.expert_offsets == nullptr) return ((long long)q.rows + 255) / 256 * ftiles;
-  return ((long long)q.rows / 256 + min(q.experts, q.rows)) * ftiles;
+  if (q.expert_offsets == nullptr) return ((long long)q.rows + rows - 1) / rows * ftiles;
+  return ((long long)q.rows / rows + min(q.experts, q.rows)) * ftiles;
 }
 
-template <typename OT>
+template <int ROWS, typename OT>
 cudaError_t launch_pair(const MxLinearParams& q, int sms, cudaStream_t stream, const char** why) {
-  typedef PairCfg C;
+  typedef PairCfg<ROWS> C;
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
@@ -1091,7 +1100,7 @@ cudaError_t launch_pair(const MxLinearParams& q, int sms, cudaStream_t stream, c
   {
     std::lock_guard<std::mutex> lk(g_mu);
     if (!attr[dev]) {
-      err = cudaFuncSetAttribute(mx_linear_pair_kernel<OT>,
+      err = cudaFuncSetAttribute(mx_linear_pair_kernel<ROWS, OT>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
       if (err != cudaSuccess) return err;
       attr[dev] = true;
@@ -1115,7 +1124,7 @@ cudaError_t launch_pair(const MxLinearParams& q, int sms, cudaStream_t stream, c
   p.scale_copy = kByTma;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attrs[1];
-  cfg.gridDim = dim3((unsigned)(2 * min((long long)sms / 2, pair_bound(q))), 1, 1);
+  cfg.gridDim = dim3((unsigned)(2 * min((long long)sms / 2, pair_bound(q, ROWS))), 1, 1);
   cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
@@ -1125,7 +1134,7 @@ cudaError_t launch_pair(const MxLinearParams& q, int sms, cudaStream_t stream, c
   attrs[0].val.clusterDim.z = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mx_linear_pair_kernel<OT>, map_w, map_x, map_ws, map_xs, p);
+  return cudaLaunchKernelEx(&cfg, mx_linear_pair_kernel<ROWS, OT>, map_w, map_x, map_ws, map_xs, p);
 }
 
 // Clusters of `size` CTAs (one to an SM) that run at once: fewer than SMs / size,
@@ -1202,8 +1211,12 @@ cudaError_t launch_typed(const MxLinearParams& q, cudaStream_t stream, const cha
   const cudaError_t err = dev_sms(&dev, &sms);
   if (err != cudaSuccess) return err;
   const Shape s = choose(q, dev, sms);
-  if (s.rows == 256 && s.splits == 1 && q.K % kBlockK == 0 && pair_bound(q) >= sms / 2)
-    return launch_pair<OT>(q, sms, stream, why);
+  if (s.splits == 1 && q.K % kBlockK == 0) {
+    if (s.rows == 256 && pair_bound(q, 256) >= sms / 2)
+      return launch_pair<256, OT>(q, sms, stream, why);
+    if (s.rows == 128 && pair_bound(q, 128) >= sms / 2)
+      return launch_pair<128, OT>(q, sms, stream, why);
+  }
   switch (s.rows) {
     case 16: return launch<16, OT>(q, s.splits, stream, why);
     case 32: return launch<32, OT>(q, s.splits, stream, why);
