@@ -5,20 +5,34 @@
 // or one per expert with the rows sorted by expert (the base grouped product of
 // a routed layer, whose output the expert fold adds to).
 //
-// D[128 features, BN rows] = W X^T: the weight is the M operand, so that the
-// row tile (N) can follow the number of rows an expert has, 16 to 128, while
-// every fetched weight tile is full.
+// D[128 features, BN rows] = W X^T: the weight is the M operand, so that the row
+// tile (N, 16 to 256) can follow the number of rows an expert has while every
+// fetched weight tile is full; a tile that an expert's end cuts short computes its
+// rows in 32s.
 //
-// Warps: 0 loads element tiles by tensor TMA (128-byte swizzled, K-major, 256
-// elements of k a stage); 2 and 3 bring the scales of the weight and x rows into
-// the order the tensor core reads (32 lanes x 4 words: row 32 j + l in word j of
-// lane l, a word being the scales of 128 elements); 1 copies those to tensor
-// memory (tcgen05.cp) and issues the MMAs (kind::mxf4, 64 elements of k each);
-// 4 to 7 drain the accumulator (two of them, so that a tile drains while the
-// next one runs).
-// With few tiles a cluster of `splits` CTAs shares one tile, each over its part
-// of k, and the partial sums are added through distributed shared memory in
-// rank order (the result does not depend on timing).
+// Warps: one loads element tiles by tensor TMA (128-byte swizzled, K-major, 256
+// elements of k a stage); one the raw scales (512 elements of k a block: 16 bytes a
+// row, by TMA, or by asynchronous copies where the rows' pitch is no multiple of
+// 16); two put those in the order the tensor core reads (32 lanes x 4 words: row
+// 32 j + l in word j of lane l, a word being the scales of 128 elements); one thread
+// copies them to tensor memory (tcgen05.cp) and issues the MMAs (kind::mxf4, 64
+// elements of k each); four or eight warps drain the accumulator (two of them up to
+// 128 rows, so that a tile drains while the next one runs), turn it with stmatrix
+// and store 16 bytes of features a lane.  The issuing thread's work per stage is
+// what the first version of this kernel spent its time on (a stage of 128 x 128
+// took 1270 cycles, 270 being the tensor core's): its descriptors are additions to
+// precomputed words.
+//
+// What bounds it.  Few rows: the weight's bytes (32 tokens x 8 of 128 experts, 2048
+// by 1536: 174 MB in 32 us, 5.2 TB/s with start and end; one row of 4096 by 28672:
+// 15.0 us, 9.6 being its 62.5 MB at the copy rate).  Where there are fewer tiles
+// than SMs a cluster of `splits` CTAs shares a tile, each over its part of k, and
+// the partial sums are added through distributed shared memory in rank order (the
+// result does not depend on timing): 128 rows of 14336 by 4096 take 13.4 us instead
+// of 18.4.  Many rows: a 128 x 256 tile of one CTA is bound by shared memory (12 KB
+// read and 12 written per MMA of 135 cycles); two CTAs on one tile of 256 x 256
+// (below) take 8 and 8: 8192 rows of 4096 by 28672 in 356 us (5.4 PFLOP/s; 408 with
+// one CTA a tile), or 415 us where it runs long enough to meet the power limit.
 //
 // Every wait is bounded; on a timeout the CTA raises LORA_FLAG_TIMEOUT, stops
 // issuing, lets its copies land, frees its tensor memory and exits.
