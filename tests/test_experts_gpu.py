@@ -244,6 +244,34 @@ def test_route_groups(score, pair, E, G, g, k):
     _check_route(x, bias, k, score=score, G=G, g=g, pair=pair, renorm=False)
 
 
+@pytest.mark.parametrize("name,score,E,k,kw", [
+    ("bf16", "sigmoid", 256, 8, dict(G=8, g=4, pair=True)), ("bf16", "softmax", 128, 6, dict()),
+    ("f32", "sigmoid", 160, 15, dict(renorm=False)), ("f16", "softmax", 72, 3, dict(scale=2.5)),
+    ("bf16", "softmax", 200, 4, dict(renorm=False)), ("f32", "softmax", 128, 8, dict(G=16, g=5)),
+    ("bf16", "sigmoid", 128, 8, dict(G=4, g=2, pair=True, renorm=False))])
+def test_route_many_tokens(name, score, E, k, kw):
+    """Several tokens a warp: masked and padded tokens, ties and close calls among
+    the rest."""
+    t = _torch()
+    rng = np.random.default_rng(E + k)
+    x = rng.standard_normal((4203, E)) * 2
+    x[7, :] = -np.inf
+    x[8, 3:] = -np.inf
+    x[100:200] = np.round(x[100:200])               # ties
+    x[4202] = 0
+    bias = rng.standard_normal(E) * 0.1
+    x = _dev(x, _dtype(name))
+    for r in range(300, 900, 50):                   # keys of one token within 2^-25 of .5 ...
+        row = _host(x)[r]
+        s = 1 / (1 + np.exp(-row)) if score == "sigmoid" else np.exp(row - row.max()) / np.exp(row - row.max()).sum()
+        close = bias.copy()
+        close[::2] = (0.5 - s)[::2]                 # (every other expert's)
+    _check_route(x, _dev(bias, t.float32), k, score=score, **kw)
+    _check_route(x, _dev(close, t.float32), k, score=score, **kw)
+    x[11, 5], x[4000, 0] = float("nan"), float("inf")
+    _check_route(x, _dev(bias, t.float32), k, score=score, **kw)
+
+
 def test_route_ties_go_to_the_lowest_index():
     t = _torch()
     for bias in (None, t.zeros(64, device="cuda")):
