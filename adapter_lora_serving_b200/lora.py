@@ -241,18 +241,23 @@ def lora_expert_apply(x_sorted, y_sorted, a, b, pair_index, ranks, scalings, row
 # the current device.  They are short (a call's host time is that of a small
 # batch's kernel), so the checks are plain loops without closures or objects.
 
-_TYPES = (LORA_TYPE_BF16, LORA_TYPE_F16, LORA_TYPE_F32)
 _torch = None      # the torch module and its element types, once a tensor is given
 _dtypes = None
+_kinds = None
 _raw_stream = None
+_current_device = None
 
 
 def _import_torch():
-    global _torch, _dtypes, _raw_stream
+    global _torch, _dtypes, _kinds, _raw_stream, _current_device
     import torch
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    # (a tensor on a CUDA device is there: no need to look whether CUDA is set up)
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _dtypes = {LORA_TYPE_BF16: torch.bfloat16, LORA_TYPE_F16: torch.float16,
                LORA_TYPE_F32: torch.float32, "int32": torch.int32, "uint8": torch.uint8}
+    _kinds = {torch.bfloat16: LORA_TYPE_BF16, torch.float16: LORA_TYPE_F16,
+              torch.float32: LORA_TYPE_F32}
     _torch = torch
     return torch
 
@@ -266,27 +271,35 @@ def _pointers(op, tensors, kinds, least, names):
     of their device (None: no tensor among them).  kinds: "int32", "uint8" or an
     LORA_TYPE_*; least: elements a tensor must have."""
     ptrs, dev = [], None
-    for i, t in enumerate(tensors):
+    dtypes = _dtypes
+    for t, kind, n in zip(tensors, kinds, least):
         if t is None or t.__class__ is int:
             ptrs.append(t)
             continue
-        if _torch is None:
+        if dtypes is None:
             _import_torch()
-        if t.dtype is not _dtypes.get(kinds[i]):
-            _refuse(op, f"{names[i]} has element type {t.dtype}")
+            dtypes = _dtypes
         d = t.get_device()
-        if d != dev:
-            if d < 0:
-                _refuse(op, f"{names[i]} is not on a CUDA device")
-            if dev is not None:
-                _refuse(op, f"{names[i]} is on device {d}, not on {dev}")
+        if dev is None:
             dev = d
-        if not t.is_contiguous():
-            _refuse(op, f"{names[i]} is not contiguous")
-        if t.numel() < least[i]:
-            _refuse(op, f"{names[i]} has {t.numel()} elements, fewer than {least[i]}")
+        if (t.dtype is not dtypes.get(kind) or d != dev or d < 0 or not t.is_contiguous()
+                or t.numel() < n):
+            _explain(op, names[len(ptrs)], t, dtypes.get(kind), dev, n)
         ptrs.append(t.data_ptr())
     return ptrs, dev
+
+
+def _explain(op, name, t, dtype, dev, least):
+    """Raises, saying what is wrong with a tensor."""
+    if t.dtype is not dtype:
+        _refuse(op, f"{name} has element type {t.dtype}")
+    if t.get_device() < 0:
+        _refuse(op, f"{name} is not on a CUDA device")
+    if t.get_device() != dev:
+        _refuse(op, f"{name} is on device {t.get_device()}, not on {dev}")
+    if not t.is_contiguous():
+        _refuse(op, f"{name} is not contiguous")
+    _refuse(op, f"{name} has {t.numel()} elements, fewer than {least}")
 
 
 def _call(fn, dev, stream, *args):
@@ -294,7 +307,7 @@ def _call(fn, dev, stream, *args):
     (None: that device's current stream); raises on a non-OK status."""
     if stream is not None and stream.__class__ is not int:
         stream = stream.cuda_stream
-    if dev is not None and dev != _torch.cuda.current_device():
+    if dev is not None and dev != _current_device():
         with _torch.cuda.device(dev):
             _check(fn(*args, _torch.cuda.current_stream().cuda_stream if stream is None
                       else stream))
@@ -310,16 +323,15 @@ def _call(fn, dev, stream, *args):
 
 def _type_of(op, name, t, given):
     """The LORA_TYPE_* of a tensor (`given` for raw pointers)."""
-    if given is None:
-        if _torch is None:
-            _import_torch()
-        dtype = getattr(t, "dtype", None)
-        for kind in _TYPES:
-            if dtype is _dtypes[kind]:
-                return kind
+    if given is not None:
+        return given
+    if _torch is None:
+        _import_torch()
+    kind = _kinds.get(getattr(t, "dtype", None))
+    if kind is None:
         _refuse(op, f"{name} has no element type of LORA_TYPE_*"
                     " (a raw pointer needs the `type` argument)")
-    return given
+    return kind
 
 
 _ROUTE = ("logits", "bias", "topk_ids", "topk_weights", "err_flags")
