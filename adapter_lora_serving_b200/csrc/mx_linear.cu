@@ -81,7 +81,7 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
-enum ScaleCopy { kByTma = 0, kBy8 = 8, kBy4 = 4, kBy1 = 1 };
+enum ScaleCopy { kByTma = 0, kBy8 = 8, kBy4 = 4, kLoaded = 1 };
 
 struct Params {
   MxLinearParams q;
@@ -89,7 +89,7 @@ struct Params {
   int splits;       // CTAs per tile (the cluster size)
   int blocks;       // 512-element blocks of the whole k
   int per_split;    // blocks of a CTA's part
-  int scale_copy;   // how scales come: kByTma, or asynchronous copies of 8 or 4 bytes, or bytes
+  int scale_copy;   // how scales come: by TMA, by asynchronous copies of 8 or 4 bytes, or loaded
 };
 
 LORA_DEV uint32_t up1024(uint32_t v) { return (v + 1023u) & ~1023u; }
@@ -274,38 +274,45 @@ LORA_DEV Tile tile_of(const Params& p, const Plan& plan, int u) {
   return t;
 }
 
-// Scales of a tile into the order the tensor core reads, in place, block after
-// block (the whole warp): lane l has rows l, l + 32, l + 64, l + 96 of an atom; word
-// c of row 32 j + l becomes word j of lane l of atom c.  (Rows past the tile's are
-// whatever the slot held: their products are not stored.)
+// Rows' scale bytes in the order the tensor core reads, into a slot (the whole warp):
+// lane l has rows l, l + 32, l + 64, l + 96 of an atom (v[atom][j]); word c of row
+// 32 j + l becomes word j of lane l of atom c.  Visible to tcgen05.cp on return.
+template <int ATOMS>
+LORA_DEV void write_ordered(uint8_t* slot, const uint4 (&v)[ATOMS][4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < ATOMS; ++h) {
+    uint8_t* dst = slot + h * kSfAtom + lane * 16;
+    constexpr int kStep = ATOMS * kSfAtom;
+    *reinterpret_cast<uint4*>(dst) = make_uint4(v[h][0].x, v[h][1].x, v[h][2].x, v[h][3].x);
+    *reinterpret_cast<uint4*>(dst + kStep) = make_uint4(v[h][0].y, v[h][1].y, v[h][2].y, v[h][3].y);
+    *reinterpret_cast<uint4*>(dst + 2 * kStep) =
+        make_uint4(v[h][0].z, v[h][1].z, v[h][2].z, v[h][3].z);
+    *reinterpret_cast<uint4*>(dst + 3 * kStep) =
+        make_uint4(v[h][0].w, v[h][1].w, v[h][2].w, v[h][3].w);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Raw scales of a tile put in order, in place, block after block.  (Rows past the
+// tile's are whatever the slot held: their products are not stored.)
 template <int ATOMS, int SLOTS, bool PAIR = false>
 LORA_DEV void order_scales(uint8_t* ring, int slot_bytes, uint64_t* raw, uint64_t* ready,
                            volatile int* stop, uint32_t* flags, int total) {
   const int lane = threadIdx.x & 31;
   Ring b;
   for (int n = 0; n < total; ++n) {
-    uint8_t* slot = ring + b.s * slot_bytes + lane * 16;
+    uint8_t* slot = ring + b.s * slot_bytes;
     if (!wait_or_stop(&raw[b.s], b.round, stop, flags)) break;
     uint4 v[ATOMS][4];
 #pragma unroll
     for (int h = 0; h < ATOMS; ++h)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        v[h][j] = *reinterpret_cast<const uint4*>(slot + (h * 128 + j * 32) * 16);
+        v[h][j] = *reinterpret_cast<const uint4*>(slot + (h * 128 + j * 32 + lane) * 16);
     __syncwarp();
-#pragma unroll
-    for (int h = 0; h < ATOMS; ++h) {
-      uint8_t* dst = slot + h * kSfAtom;
-      constexpr int kStep = ATOMS * kSfAtom;
-      *reinterpret_cast<uint4*>(dst) = make_uint4(v[h][0].x, v[h][1].x, v[h][2].x, v[h][3].x);
-      *reinterpret_cast<uint4*>(dst + kStep) = make_uint4(v[h][0].y, v[h][1].y, v[h][2].y, v[h][3].y);
-      *reinterpret_cast<uint4*>(dst + 2 * kStep) =
-          make_uint4(v[h][0].z, v[h][1].z, v[h][2].z, v[h][3].z);
-      *reinterpret_cast<uint4*>(dst + 3 * kStep) =
-          make_uint4(v[h][0].w, v[h][1].w, v[h][2].w, v[h][3].w);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
+    write_ordered<ATOMS>(slot, v);
     if (lane == 0) {
       if (PAIR) arrive_at_first(&ready[b.s]);
       else mbar_arrive(&ready[b.s]);
@@ -332,21 +339,75 @@ LORA_DEV void copy_scale_rows(uint8_t* slot, const uint8_t* src, long long row0,
   }
   cp_async_arrive_noinc(raw);
 }
-// Any pitch: byte by byte, through registers.
-template <int ROWS>
-LORA_DEV void copy_scale_bytes(uint8_t* slot, const uint8_t* src, long long row0, long long nrows,
-                               int per_row, int at, uint64_t* raw) {
-  const int lane = threadIdx.x & 31;
-  for (int r = lane; r < ROWS; r += 32) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    const uint8_t* s = src + (row0 + r) * per_row + at;
-    const int n = row0 + r < nrows ? min(16, per_row - at) : 0;
+
+// The 16 scale bytes of a row from byte `at` on, at any alignment, zeros past the
+// row's end (and for rows past the last): whole words around them, shifted into
+// place.  `end`: the array's end, past which nothing is read.
+LORA_DEV uint4 load_scale_row(const uint8_t* src, const uint8_t* end, long long row, long long nrows,
+                              int per_row, int at) {
+  const int n = row < nrows ? min(16, per_row - at) : 0;
+  if (n <= 0) return make_uint4(0u, 0u, 0u, 0u);
+  const uint8_t* s = src + row * per_row + at;
+  const uint32_t shift = (uint32_t)(reinterpret_cast<uintptr_t>(s) & 3u) * 8u;
+  const uint8_t* first = s - shift / 8u;
+  uint32_t w[5];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) w[i >> 2] |= (uint32_t)__ldg(s + i) << (8 * (i & 3));
-    *reinterpret_cast<uint4*>(slot + r * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 5; ++i) {
+    w[i] = 0u;
+    const uint8_t* word = first + 4 * i;
+    if (word < s + n) {
+      if (word + 4 <= end) {
+        w[i] = __ldg(reinterpret_cast<const uint32_t*>(word));
+      } else {
+        for (int k = 0; k < 4; ++k)
+          if (word + k < end) w[i] |= (uint32_t)__ldg(word + k) << (8 * k);
+      }
+    }
   }
-  mbar_arrive(raw);
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = __funnelshift_r(w[i], w[i + 1], shift);
+    const int keep = n - 4 * i;   // bytes of this word that are the row's
+    if (keep < 4) v[i] &= keep <= 0 ? 0u : (1u << (8 * keep)) - 1u;
+  }
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// order_scales for rows whose pitch is no multiple of four: the warp loads its rows
+// itself, a block ahead, and writes them in order.
+template <int ATOMS, int ROWS, int SLOTS, typename RowOf>
+LORA_DEV void load_and_order_scales(uint8_t* ring, int slot_bytes, uint64_t* ready, uint64_t* empty,
+                                    volatile int* stop, uint32_t* flags, int units, int blocks,
+                                    int block0, RowOf row_of, const uint8_t* src, long long nrows,
+                                    int per_row) {
+  const int lane = threadIdx.x & 31;
+  const uint8_t* end = src + nrows * per_row;
+  uint4 v[ATOMS][4];
+  long long row = 0;
+  auto load = [&](int unit, int block) {
+    if (block == 0) row = (long long)row_of(unit) + lane;
+#pragma unroll
+    for (int h = 0; h < ATOMS; ++h)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[h][j] = h * 128 + j * 32 < ROWS
+                      ? load_scale_row(src, end, row + h * 128 + j * 32, nrows, per_row,
+                                       (block0 + block) * (kBlockK / 32))
+                      : make_uint4(0u, 0u, 0u, 0u);
+  };
+  Ring b;
+  bool ok = true;
+  if (units > 0) load(0, 0);
+  for (int i = 0; i < units && ok; ++i)
+    for (int k = 0; k < blocks; ++k) {
+      if (!(ok = wait_or_stop(&empty[b.s], b.round ^ 1u, stop, flags))) break;
+      write_ordered<ATOMS>(ring + b.s * slot_bytes, v);
+      if (lane == 0) mbar_arrive(&ready[b.s]);
+      b.next<SLOTS>();
+      if (k + 1 < blocks) load(i, k + 1);
+      else if (i + 1 < units) load(i + 1, 0);
+    }
 }
 
 // 16 lanes x 32 columns of fp32 from tensor memory in the layout of a matrix
@@ -554,18 +615,30 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     // ---- scales into the tensor core's order: warp 2 the weight's 128 rows, warp
     // 3 those of x.  Lane l has rows l, l + 32, l + 64, l + 96 of an atom; a row's
     // 16 bytes are one word for each of four atoms. ----
-    if (warp == 2)
+    if (p.scale_copy == kLoaded) {
+      if (warp == 2)
+        load_and_order_scales<1, kM, C::kSfSlots>(
+            sf_ring, C::kSfSlot, sf_full, sf_empty, stop, p.q.flags, units, blocks, block0,
+            [&](int i) { return tile_of<BN>(p, plan, first_unit + i * unit_step).wrow; },
+            p.q.w_scales, (long long)p.q.experts * p.q.N, p.q.K / 32);
+      else
+        load_and_order_scales<C::kAtoms, BN, C::kSfSlots>(
+            sf_ring + 4 * kSfAtom, C::kSfSlot, sf_full, sf_empty, stop, p.q.flags, units, blocks,
+            block0, [&](int i) { return tile_of<BN>(p, plan, first_unit + i * unit_step).row0; },
+            p.q.x_scales, (long long)p.q.rows, p.q.K / 32);
+    } else if (warp == 2) {
       order_scales<1, C::kSfSlots>(sf_ring, C::kSfSlot, sf_raw, sf_full, stop, p.q.flags,
                                    units * blocks);
-    else
+    } else {
       order_scales<C::kAtoms, C::kSfSlots>(sf_ring + 4 * kSfAtom, C::kSfSlot, sf_raw + C::kSfSlots,
                                            sf_full, stop, p.q.flags, units * blocks);
+    }
   } else if (warp == 4 + C::kEpiWarps) {
     // ---- raw scales ----
     const bool by_tma = p.scale_copy == kByTma;
     const int per_row = p.q.K / 32;
     const long long w_rows = (long long)p.q.experts * p.q.N;
-    if (!by_tma || elect_one()) {
+    if (p.scale_copy != kLoaded && (!by_tma || elect_one())) {
       Ring b;
       bool ok = true;
       for (int i = 0; i < units && ok; ++i) {
@@ -584,12 +657,9 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
           } else if (p.scale_copy == kBy8) {
             copy_scale_rows<8, kM>(w, p.q.w_scales, t.wrow, w_rows, per_row, at, raw_w);
             copy_scale_rows<8, BN>(x, p.q.x_scales, t.row0, p.q.rows, per_row, at, raw_x);
-          } else if (p.scale_copy == kBy4) {
+          } else {
             copy_scale_rows<4, kM>(w, p.q.w_scales, t.wrow, w_rows, per_row, at, raw_w);
             copy_scale_rows<4, BN>(x, p.q.x_scales, t.row0, p.q.rows, per_row, at, raw_x);
-          } else {
-            copy_scale_bytes<kM>(w, p.q.w_scales, t.wrow, w_rows, per_row, at, raw_w);
-            copy_scale_bytes<BN>(x, p.q.x_scales, t.row0, p.q.rows, per_row, at, raw_x);
           }
           b.next<C::kSfSlots>();
         }
@@ -1101,7 +1171,7 @@ cudaError_t launch(const MxLinearParams& q, int splits, cudaStream_t stream, con
   p.blocks = (q.K + kBlockK - 1) / kBlockK;
   p.per_split = (p.blocks + splits - 1) / splits;
   p.splits = (p.blocks + p.per_split - 1) / p.per_split;   // every CTA has a part
-  p.scale_copy = q.K % kBlockK == 0 ? kByTma : q.K % 256 == 0 ? kBy8 : q.K % 128 == 0 ? kBy4 : kBy1;
+  p.scale_copy = q.K % kBlockK == 0 ? kByTma : q.K % 256 == 0 ? kBy8 : q.K % 128 == 0 ? kBy4 : kLoaded;
   if (p.scale_copy == kByTma) {
     err = make_map(&map_ws, q.w_scales, (uint64_t)q.K / 32, w_rows, kBlockK / 32, kM, why);
     if (err != cudaSuccess) return err;
@@ -1227,7 +1297,10 @@ Shape choose(const MxLinearParams& q, int dev, int sms) {
     while (s > 1 && clusters_at_once(dev, s) < tiles) --s;
     return max(1, s);
   };
-  Shape best = {mean <= 16 ? 16 : mean <= 32 ? 32 : mean <= 64 ? 64 : 128, 1};
+  // (with few k a tile's epilogue weighs more, and wider tiles are fewer: 512 x 8 rows
+  // of 128 experts, 768 by 2048: 33.9 us with 64 rows a tile, 40.2 with 32)
+  const long long fit = q.K <= 1024 && experts > 1 ? 2 * mean : mean;
+  Shape best = {fit <= 16 ? 16 : fit <= 32 ? 32 : fit <= 64 ? 64 : 128, 1};
   best.splits = splits_for(tile_bound(q, best.rows));
   if (mean <= 128) return best;
   if (q.expert_offsets != nullptr) return {256, splits_for(tile_bound(q, 256))};
