@@ -65,10 +65,12 @@ struct Cfg {
   static constexpr int kBTile = BN * kK / 2;
   static constexpr int kStage = kATile + kBTile;
   static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : BN >= 64 ? 8 : BN >= 32 ? 9 : 8;
-  static constexpr int kSfSlots = BN >= 256 ? 3 : BN >= 64 ? 5 : 6;   // blocks of scales in flight
+  static constexpr int kSfSlots = BN >= 256 ? 3 : BN >= 64 ? 4 : 5;   // blocks of scales in flight
   static constexpr int kAtoms = BN > 128 ? 2 : 1;             // of x, per 128 elements of k
-  static constexpr int kSfX = 4 * kAtoms * kSfAtom;
-  static constexpr int kSfSlot = 4 * kSfAtom + kSfX;
+  // a slot: raw rows of 16 bytes, or (up to 128 rows) of the 20 around 16 unaligned
+  // ones, W's then X's; put in order in place
+  static constexpr int kSfX0 = BN > 128 ? 4 * kSfAtom : kM * 20;
+  static constexpr int kSfSlot = BN > 128 ? 12 * kSfAtom : 2 * kM * 20;
   static constexpr int kAcc = BN > 128 ? 1 : 2;               // accumulators
   static constexpr int kSfCols = 16 + 16 * kAtoms;            // tensor memory columns of a block of scales
   static constexpr int kUsed = kAcc * BN + 2 * kSfCols;
@@ -81,7 +83,7 @@ struct Cfg {
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
-enum ScaleCopy { kByTma = 0, kBy8 = 8, kBy4 = 4, kLoaded = 1 };
+enum ScaleCopy { kByTma = 0, kBy8 = 8, kBy4 = 4, kAround = 1 };
 
 struct Params {
   MxLinearParams q;
@@ -89,7 +91,8 @@ struct Params {
   int splits;       // CTAs per tile (the cluster size)
   int blocks;       // 512-element blocks of the whole k
   int per_split;    // blocks of a CTA's part
-  int scale_copy;   // how scales come: by TMA, by asynchronous copies of 8 or 4 bytes, or loaded
+  int scale_copy;   // how scales come: by TMA, by asynchronous copies of 8 or 4 bytes, or of the
+                    // words around them
 };
 
 LORA_DEV uint32_t up1024(uint32_t v) { return (v + 1023u) & ~1023u; }
@@ -340,74 +343,64 @@ LORA_DEV void copy_scale_rows(uint8_t* slot, const uint8_t* src, long long row0,
   cp_async_arrive_noinc(raw);
 }
 
-// The 16 scale bytes of a row from byte `at` on, at any alignment, zeros past the
-// row's end (and for rows past the last): whole words around them, shifted into
-// place.  `end`: the array's end, past which nothing is read.
-LORA_DEV uint4 load_scale_row(const uint8_t* src, const uint8_t* end, long long row, long long nrows,
-                              int per_row, int at) {
-  const int n = row < nrows ? min(16, per_row - at) : 0;
-  if (n <= 0) return make_uint4(0u, 0u, 0u, 0u);
-  const uint8_t* s = src + row * per_row + at;
-  const uint32_t shift = (uint32_t)(reinterpret_cast<uintptr_t>(s) & 3u) * 8u;
-  const uint8_t* first = s - shift / 8u;
-  uint32_t w[5];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) {
-    w[i] = 0u;
-    const uint8_t* word = first + 4 * i;
-    if (word < s + n) {
-      if (word + 4 <= end) {
-        w[i] = __ldg(reinterpret_cast<const uint32_t*>(word));
-      } else {
-        for (int k = 0; k < 4; ++k)
-          if (word + k < end) w[i] |= (uint32_t)__ldg(word + k) << (8 * k);
-      }
-    }
+// The same for any pitch: the five aligned words around a row's 16 bytes, to rows of
+// 20.  Nothing past `end`, the array's, is read.
+template <int ROWS>
+LORA_DEV void copy_scale_words(uint8_t* slot, const uint8_t* src, const uint8_t* end, long long row0,
+                               long long nrows, int per_row, int at, uint64_t* raw) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 4
+  for (int i = lane; i < ROWS * 5; i += 32) {
+    const int r = i / 5, o = i % 5 * 4;
+    const uint8_t* s = src + (row0 + r) * per_row + at;
+    const uint8_t* word = s - (reinterpret_cast<uintptr_t>(s) & 3u) + o;
+    const int n = row0 + r < nrows && word < end ? (int)min(4LL, (long long)(end - word)) : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(slot + r * 20 + o)),
+                 "l"(n > 0 ? word : src), "r"(n)
+                 : "memory");
   }
-  uint32_t v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = __funnelshift_r(w[i], w[i + 1], shift);
-    const int keep = n - 4 * i;   // bytes of this word that are the row's
-    if (keep < 4) v[i] &= keep <= 0 ? 0u : (1u << (8 * keep)) - 1u;
-  }
-  return make_uint4(v[0], v[1], v[2], v[3]);
+  cp_async_arrive_noinc(raw);
 }
 
-// order_scales for rows whose pitch is no multiple of four: the warp loads its rows
-// itself, a block ahead, and writes them in order.
-template <int ATOMS, int ROWS, int SLOTS, typename RowOf>
-LORA_DEV void load_and_order_scales(uint8_t* ring, int slot_bytes, uint64_t* ready, uint64_t* empty,
-                                    volatile int* stop, uint32_t* flags, int units, int blocks,
-                                    int block0, RowOf row_of, const uint8_t* src, long long nrows,
-                                    int per_row) {
+// order_scales for those: the words are shifted into place, and what is past a row's
+// end cleared.
+template <int ROWS, int SLOTS, typename RowOf>
+LORA_DEV void order_scale_words(uint8_t* ring, int slot_bytes, uint64_t* raw, uint64_t* ready,
+                                volatile int* stop, uint32_t* flags, int units, int blocks,
+                                int block0, RowOf row_of, const uint8_t* src, int per_row) {
   const int lane = threadIdx.x & 31;
-  const uint8_t* end = src + nrows * per_row;
-  uint4 v[ATOMS][4];
-  long long row = 0;
-  auto load = [&](int unit, int block) {
-    if (block == 0) row = (long long)row_of(unit) + lane;
-#pragma unroll
-    for (int h = 0; h < ATOMS; ++h)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[h][j] = h * 128 + j * 32 < ROWS
-                      ? load_scale_row(src, end, row + h * 128 + j * 32, nrows, per_row,
-                                       (block0 + block) * (kBlockK / 32))
-                      : make_uint4(0u, 0u, 0u, 0u);
-  };
   Ring b;
   bool ok = true;
-  if (units > 0) load(0, 0);
-  for (int i = 0; i < units && ok; ++i)
+  for (int i = 0; i < units && ok; ++i) {
+    const long long row = (long long)row_of(i) + lane;
     for (int k = 0; k < blocks; ++k) {
-      if (!(ok = wait_or_stop(&empty[b.s], b.round ^ 1u, stop, flags))) break;
-      write_ordered<ATOMS>(ring + b.s * slot_bytes, v);
+      const int at = (block0 + k) * (kBlockK / 32);
+      uint8_t* slot = ring + b.s * slot_bytes;
+      if (!(ok = wait_or_stop(&raw[b.s], b.round, stop, flags))) break;
+      uint4 v[1][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[0][j] = make_uint4(0u, 0u, 0u, 0u);
+        if (j * 32 + lane < ROWS) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(slot + (j * 32 + lane) * 20);
+          const uint32_t shift =
+              (uint32_t)((reinterpret_cast<uintptr_t>(src) + (row + j * 32) * per_row + at) & 3) * 8u;
+          uint32_t x[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            x[c] = __funnelshift_r(w[c], w[c + 1], shift);
+            const int keep = per_row - at - 4 * c;   // bytes of this word that are the row's
+            if (keep < 4) x[c] &= keep <= 0 ? 0u : (1u << (8 * keep)) - 1u;
+          }
+          v[0][j] = make_uint4(x[0], x[1], x[2], x[3]);
+        }
+      }
+      __syncwarp();
+      write_ordered<1>(slot, v);
       if (lane == 0) mbar_arrive(&ready[b.s]);
       b.next<SLOTS>();
-      if (k + 1 < blocks) load(i, k + 1);
-      else if (i + 1 < units) load(i + 1, 0);
     }
+  }
 }
 
 // 16 lanes x 32 columns of fp32 from tensor memory in the layout of a matrix
@@ -586,7 +579,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
 #pragma unroll
               for (int h = 0; h < C::kAtoms; ++h)
                 copy_scales(sf + 16 + 4 * (C::kAtoms * c + h),
-                            lo + (4 + C::kAtoms * c + h) * (kSfAtom >> 4));
+                            lo + (C::kSfX0 >> 4) + (C::kAtoms * c + h) * (kSfAtom >> 4));
             }
             mma_commit(&sf_empty[b.s]);
             b.next<C::kSfSlots>();
@@ -615,22 +608,23 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     // ---- scales into the tensor core's order: warp 2 the weight's 128 rows, warp
     // 3 those of x.  Lane l has rows l, l + 32, l + 64, l + 96 of an atom; a row's
     // 16 bytes are one word for each of four atoms. ----
-    if (p.scale_copy == kLoaded) {
+    if (BN <= 128 && p.scale_copy == kAround) {
       if (warp == 2)
-        load_and_order_scales<1, kM, C::kSfSlots>(
-            sf_ring, C::kSfSlot, sf_full, sf_empty, stop, p.q.flags, units, blocks, block0,
+        order_scale_words<kM, C::kSfSlots>(
+            sf_ring, C::kSfSlot, sf_raw, sf_full, stop, p.q.flags, units, blocks, block0,
             [&](int i) { return tile_of<BN>(p, plan, first_unit + i * unit_step).wrow; },
-            p.q.w_scales, (long long)p.q.experts * p.q.N, p.q.K / 32);
+            p.q.w_scales, p.q.K / 32);
       else
-        load_and_order_scales<C::kAtoms, BN, C::kSfSlots>(
-            sf_ring + 4 * kSfAtom, C::kSfSlot, sf_full, sf_empty, stop, p.q.flags, units, blocks,
-            block0, [&](int i) { return tile_of<BN>(p, plan, first_unit + i * unit_step).row0; },
-            p.q.x_scales, (long long)p.q.rows, p.q.K / 32);
+        order_scale_words<BN, C::kSfSlots>(
+            sf_ring + C::kSfX0, C::kSfSlot, sf_raw + C::kSfSlots, sf_full, stop, p.q.flags, units,
+            blocks, block0,
+            [&](int i) { return tile_of<BN>(p, plan, first_unit + i * unit_step).row0; },
+            p.q.x_scales, p.q.K / 32);
     } else if (warp == 2) {
       order_scales<1, C::kSfSlots>(sf_ring, C::kSfSlot, sf_raw, sf_full, stop, p.q.flags,
                                    units * blocks);
     } else {
-      order_scales<C::kAtoms, C::kSfSlots>(sf_ring + 4 * kSfAtom, C::kSfSlot, sf_raw + C::kSfSlots,
+      order_scales<C::kAtoms, C::kSfSlots>(sf_ring + C::kSfX0, C::kSfSlot, sf_raw + C::kSfSlots,
                                            sf_full, stop, p.q.flags, units * blocks);
     }
   } else if (warp == 4 + C::kEpiWarps) {
@@ -638,7 +632,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     const bool by_tma = p.scale_copy == kByTma;
     const int per_row = p.q.K / 32;
     const long long w_rows = (long long)p.q.experts * p.q.N;
-    if (p.scale_copy != kLoaded && (!by_tma || elect_one())) {
+    if (!by_tma || elect_one()) {
       Ring b;
       bool ok = true;
       for (int i = 0; i < units && ok; ++i) {
@@ -646,7 +640,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
         for (int k = 0; k < blocks; ++k) {
           if (!(ok = wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags))) break;
           uint8_t* w = sf_ring + b.s * C::kSfSlot;
-          uint8_t* x = w + 4 * kSfAtom;
+          uint8_t* x = w + C::kSfX0;
           uint64_t *raw_w = &sf_raw[b.s], *raw_x = &sf_raw[C::kSfSlots + b.s];
           const int at = k0 / 32 + k * (kBlockK / 32);
           if (by_tma) {
@@ -657,9 +651,14 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
           } else if (p.scale_copy == kBy8) {
             copy_scale_rows<8, kM>(w, p.q.w_scales, t.wrow, w_rows, per_row, at, raw_w);
             copy_scale_rows<8, BN>(x, p.q.x_scales, t.row0, p.q.rows, per_row, at, raw_x);
-          } else {
+          } else if (p.scale_copy == kBy4) {
             copy_scale_rows<4, kM>(w, p.q.w_scales, t.wrow, w_rows, per_row, at, raw_w);
             copy_scale_rows<4, BN>(x, p.q.x_scales, t.row0, p.q.rows, per_row, at, raw_x);
+          } else if (BN <= 128) {
+            copy_scale_words<kM>(w, p.q.w_scales, p.q.w_scales + w_rows * per_row, t.wrow, w_rows,
+                                 per_row, at, raw_w);
+            copy_scale_words<BN>(x, p.q.x_scales, p.q.x_scales + (long long)p.q.rows * per_row,
+                                 t.row0, p.q.rows, per_row, at, raw_x);
           }
           b.next<C::kSfSlots>();
         }
@@ -1171,7 +1170,7 @@ cudaError_t launch(const MxLinearParams& q, int splits, cudaStream_t stream, con
   p.blocks = (q.K + kBlockK - 1) / kBlockK;
   p.per_split = (p.blocks + splits - 1) / splits;
   p.splits = (p.blocks + p.per_split - 1) / p.per_split;   // every CTA has a part
-  p.scale_copy = q.K % kBlockK == 0 ? kByTma : q.K % 256 == 0 ? kBy8 : q.K % 128 == 0 ? kBy4 : kLoaded;
+  p.scale_copy = q.K % kBlockK == 0 ? kByTma : q.K % 256 == 0 ? kBy8 : q.K % 128 == 0 ? kBy4 : kAround;
   if (p.scale_copy == kByTma) {
     err = make_map(&map_ws, q.w_scales, (uint64_t)q.K / 32, w_rows, kBlockK / 32, kM, why);
     if (err != cudaSuccess) return err;
@@ -1302,7 +1301,7 @@ Shape choose(const MxLinearParams& q, int dev, int sms) {
   const long long fit = q.K <= 1024 && experts > 1 ? 2 * mean : mean;
   Shape best = {fit <= 16 ? 16 : fit <= 32 ? 32 : fit <= 64 ? 64 : 128, 1};
   best.splits = splits_for(tile_bound(q, best.rows));
-  if (mean <= 128) return best;
+  if (mean <= 128 || q.K % 128 != 0) return best;   // (256 rows: no room for unaligned scales)
   if (q.expert_offsets != nullptr) return {256, splits_for(tile_bound(q, 256))};
   double least = 0;
   for (int bn = 128; bn <= 256; bn += 128) {
