@@ -349,15 +349,22 @@ template <int ROWS>
 LORA_DEV void copy_scale_words(uint8_t* slot, const uint8_t* src, const uint8_t* end, long long row0,
                                long long nrows, int per_row, int at, uint64_t* raw) {
   const int lane = threadIdx.x & 31;
-#pragma unroll 4
-  for (int i = lane; i < ROWS * 5; i += 32) {
-    const int r = i / 5, o = i % 5 * 4;
-    const uint8_t* s = src + (row0 + r) * per_row + at;
-    const uint8_t* word = s - (reinterpret_cast<uintptr_t>(s) & 3u) + o;
-    const int n = row0 + r < nrows && word < end ? (int)min(4LL, (long long)(end - word)) : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(slot + r * 20 + o)),
-                 "l"(n > 0 ? word : src), "r"(n)
-                 : "memory");
+#pragma unroll
+  for (int j = 0; j < (ROWS + 31) / 32; ++j) {
+    const int r = j * 32 + lane;
+    if (r < ROWS) {
+      const uint8_t* s = src + (row0 + r) * per_row + at;
+      const uint8_t* first = s - (reinterpret_cast<uintptr_t>(s) & 3u);
+      const long long left = row0 + r < nrows ? end - first : 0;
+      const uint32_t to = smem_u32(slot + r * 20);
+#pragma unroll
+      for (int o = 0; o < 20; o += 4) {
+        const int n = (int)max(0LL, min(4LL, left - o));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + o),
+                     "l"(n > 0 ? first + o : src), "r"(n)
+                     : "memory");
+      }
+    }
   }
   cp_async_arrive_noinc(raw);
 }
