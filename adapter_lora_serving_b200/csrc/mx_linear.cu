@@ -88,6 +88,7 @@ enum ScaleCopy { kByTma = 0, kBy8 = 8, kBy4 = 4, kAround = 1 };
 struct Params {
   MxLinearParams q;
   int ftiles;       // feature tiles of a weight
+  int most;         // tiles that offsets which do not overlap can make
   int splits;       // CTAs per tile (the cluster size)
   int blocks;       // 512-element blocks of the whole k
   int per_split;    // blocks of a CTA's part
@@ -253,6 +254,23 @@ LORA_DEV Plan make_plan(const Params& p, int* prefix, int* scratch) {
     const int inc = block_inclusive_scan<THREADS>(cnt, scratch, &tot);
     if (e < p.q.experts) prefix[e + 1] = plan.tiles + inc;
     plan.tiles += tot;
+  }
+  if (__syncthreads_or(bad != 0)) {
+    // Offsets that go back can make blocks overlap, and more tiles than there is
+    // room for: counted again one by one, leaving out experts beyond that.
+    if (threadIdx.x == 0) {
+      int tiles = 0;
+      for (int e = 0; e < p.q.experts; ++e) {
+        const int lo = plan.offsets[e], hi = plan.offsets[e + 1];
+        if (lo >= 0 && hi <= p.q.rows && hi >= lo) {
+          const long long cnt = (long long)((hi - lo + BN - 1) / BN) * p.ftiles;
+          if (tiles + cnt <= p.most) tiles += (int)cnt;
+        }
+        prefix[e + 1] = tiles;
+      }
+    }
+    __syncthreads();
+    plan.tiles = prefix[p.q.experts];
   }
   if (blockIdx.x == 0) raise_flag(p.q.flags, bad);
   return plan;
@@ -1176,6 +1194,7 @@ cudaError_t launch(const MxLinearParams& q, int splits, cudaStream_t stream, con
   p.ftiles = (q.N + kM - 1) / kM;
   p.blocks = (q.K + kBlockK - 1) / kBlockK;
   p.per_split = (p.blocks + splits - 1) / splits;
+  p.most = (int)tile_bound(q, BN);
   p.splits = (p.blocks + p.per_split - 1) / p.per_split;   // every CTA has a part
   p.scale_copy = q.K % kBlockK == 0 ? kByTma : q.K % 256 == 0 ? kBy8 : q.K % 128 == 0 ? kBy4 : kAround;
   if (p.scale_copy == kByTma) {
@@ -1238,6 +1257,7 @@ cudaError_t launch_pair(const MxLinearParams& q, int sms, cudaStream_t stream, c
   p.q = q;
   p.ftiles = (q.N + 2 * kM - 1) / (2 * kM);
   p.splits = 1;
+  p.most = (int)pair_bound(q, ROWS);
   p.blocks = p.per_split = q.K / kBlockK;
   p.scale_copy = kByTma;
   cudaLaunchConfig_t cfg = {};

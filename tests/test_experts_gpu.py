@@ -547,3 +547,38 @@ def test_expert_linear_padding_and_types():
 def test_expert_linear_bad_offsets_skip_the_expert():
     _check_expert("bf16", [10, 20, 30], 128, 64, offsets=np.array([-3, 10, 30, 70]))
     _check_expert("bf16", [10, 20, 30], 128, 64, offsets=np.array([0, 30, 10, 60]))
+
+
+def test_expert_linear_offsets_that_go_back_and_forth():
+    """Offsets 0, rows, 0, rows, ...: every other expert claims all rows.  Flagged;
+    the rows' values are unspecified, but only rows of y are written."""
+    t = _torch()
+    rng = np.random.default_rng(4)
+    E, rows, K, N = 64, 100, 512, 256
+    xc, xs, _ = _operand(rng, rows, K)
+    wc, ws, _ = _operand(rng, E, N, K)
+    y = t.full((rows + 40, N), 7.0, device="cuda")
+    flags = _flags()
+    L.lora_mx_expert_linear(xc, xs, wc, ws, _i32(np.arange(E + 1) % 2 * rows), y, rows, K, N, E,
+                            err_flags=flags)
+    assert (y[rows:] == 7.0).all() and int(flags.item()) == L.LORA_FLAG_BAD_OFFSETS
+
+
+@pytest.mark.parametrize("rows,K,N", [(40, 512, 136), (5, 2048, 128), (700, 1056, 4096), (2304, 512, 2304)])
+def test_linear_nan_scale_stays_in_its_row(rows, K, N):
+    """A block without a scale (byte 255) makes its row (of x) or feature (of w) NaN
+    and nothing else."""
+    t = _torch()
+    rng = np.random.default_rng(rows)
+    xc, xs, x = _operand(rng, rows, K, spread=0.5)
+    wc, ws, w = _operand(rng, N, K, spread=0.5)
+    xs[3, K // 32 - 1] = 255
+    ws[N - 2, 1] = 255
+    y = t.empty(rows, N, device="cuda")
+    L.lora_mx_linear(xc, xs, wc, ws, y, rows, K, N)
+    got = _host(y)
+    assert np.isnan(got[3]).all() and np.isnan(got[:, N - 2]).all()
+    keep = np.ones((rows, N), dtype=bool)
+    keep[3], keep[:, N - 2] = False, False
+    ref, mag = O.mx_linear(x, w)
+    _close(got[keep], ref[keep], _tol("f32", K, mag, ref)[keep], "beside NaN")
