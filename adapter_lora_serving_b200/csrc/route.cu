@@ -191,9 +191,9 @@ struct Exact {
 //     sum by 2.5 u and half a u for each of VPL + 5 additions, the quotient and the
 //     product by 2.5 u more: (8 + (VPL + 5) / 2) u smax.
 //   the bias sum: half a u of the key; the place within the lane that fills its
-//     four lowest bits (Sorted): 7.5 u of it.
+//     three lowest bits (Sorted): 7 u of it.  Two keys: 15 u, here 16.
 // A pair's sum has the errors of both its keys, whose magnitudes its own can be
-// far below: `of_sum` has the row's largest.
+// far below, and half a u for the sum: 31 u of the row's largest key, here 34.
 struct Within {
   static constexpr bool kExact = false;
   float of_score;
@@ -333,8 +333,8 @@ LORA_DEV void sort_network(Swap order) {
 // network, after which a round of the selection looks at the lanes' first keys
 // alone (the list of the lane that gave one moves up).  Equal keys stay in order of
 // their places.  Where the place in the lane is held:
-//   kLow    in the key's four lowest bits (15 - i), which changes an approximate
-//           key by 15 ulps at most (accounted for in Within);
+//   kLow    in the key's three lowest bits (7 - i), which moves an approximate key by
+//           7 ulps at most (accounted for in Within);
 //   kExpert in the ten lowest bits (1023 - e) of a 16-bit logit's key, whose own
 //           lowest 13 are constant: exact, and no two are equal;
 //   kBeside beside the key: exact keys that need all their bits.
@@ -363,7 +363,7 @@ struct Sorted {
     } else {
 #pragma unroll
       for (int i = 0; i < VPL; ++i)
-        u[i] = kPlace == kLow ? (u[i] & ~(U)15) | (U)(15 - i)
+        u[i] = kPlace == kLow ? (u[i] & ~(U)7) | (U)(7 - i)
                               : (u[i] & ~(U)1023) | (U)(1023 - (lane * VPL + i));
       sort_network<VPL>([&](int i, int j) {
         const U hi = max(u[i], u[j]);
@@ -415,7 +415,7 @@ struct Sorted {
   LORA_DEV int expert(U key, int from, int place) const {
     if (!is_open(key)) return -1;
     if (kAt) return from * VPL + place;
-    if (kPlace == kLow) return from * VPL + 15 - (int)((uint32_t)key & 15u);
+    if (kPlace == kLow) return from * VPL + 7 - (int)((uint32_t)key & 7u);
     return 1023 - (int)((uint32_t)key & 1023u);
   }
 

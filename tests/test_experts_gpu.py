@@ -302,6 +302,19 @@ def test_route_close_scores_as_in_64_bits():
         _check_route(_dev(x, t.float32), _dev(bias, t.float32), 4, G=8, g=2, pair=True)
 
 
+def test_route_keys_a_few_steps_apart():
+    """Equal small scores and biases 18 (and 9) fp32 steps apart, in an order that
+    has nothing to do with the experts': every neighbour counts."""
+    t = _torch()
+    rng = np.random.default_rng(8)
+    for E in (256, 128, 64):
+        x = np.zeros((16, E))
+        for step in (18, 9, 25):
+            for score, kw in (("softmax", {}), ("sigmoid", {}), ("softmax", dict(G=8, g=3, pair=True))):
+                bias = 1.0 + step * rng.permutation(E) * 2.0 ** -23
+                _check_route(_dev(x, t.float32), _dev(bias, t.float32), 8, score=score, **kw)
+
+
 def test_route_masked_and_nonfinite():
     t = _torch()
     inf, nan = np.inf, np.nan
