@@ -595,3 +595,36 @@ def test_linear_nan_scale_stays_in_its_row(rows, K, N):
     keep[3], keep[:, N - 2] = False, False
     ref, mag = O.mx_linear(x, w)
     _close(got[keep], ref[keep], _tol("f32", K, mag, ref)[keep], "beside NaN")
+
+
+def test_products_of_two_streams_at_once():
+    """Pair tiles, split tiles and experts' tiles in flight together on two streams
+    give the bits of each alone."""
+    t = _torch()
+    rng = np.random.default_rng(12)
+    calls = []
+    for rows, K, N, E in ((2304, 512, 2304, 0), (3, 4096, 256, 0), (160, 1056, 264, 0), (500, 768, 520, 9)):
+        xc, xs, _ = _operand(rng, rows, K)
+        wc, ws, _ = _operand(rng, max(E, 1) * N, K)
+        off = _i32(np.linspace(0, rows, E + 1).astype(int)) if E else None
+
+        def call(y, rows=rows, K=K, N=N, E=E, a=(xc, xs, wc, ws), off=off, flags=None):
+            if E:
+                L.lora_mx_expert_linear(*a, off, y, rows, K, N, E, err_flags=flags)
+            else:
+                L.lora_mx_linear(*a, y, rows, K, N, err_flags=flags)
+        want = t.empty(rows, N, dtype=t.bfloat16, device="cuda")
+        call(want)
+        calls.append((call, want))
+    flags = _flags()
+    streams = [t.cuda.Stream(), t.cuda.Stream()]
+    outs = [[t.empty_like(w) for _ in range(10)] for _, w in calls]
+    t.cuda.synchronize()
+    for j in range(10):
+        for i, (call, _) in enumerate(calls):
+            with t.cuda.stream(streams[(i + j) % 2]):
+                call(outs[i][j], flags=flags)
+    t.cuda.synchronize()
+    for out, (_, w) in zip(outs, calls):
+        assert all(t.equal(o, w) for o in out)
+    assert int(flags.item()) == 0
