@@ -349,14 +349,24 @@ template <int N, int ROWS>
 LORA_DEV void copy_scale_rows(uint8_t* slot, const uint8_t* src, long long row0, long long nrows,
                               int per_row, int at, uint64_t* raw) {
   const int lane = threadIdx.x & 31;
-#pragma unroll 4
-  for (int i = lane; i < ROWS * (16 / N); i += 32) {
-    const int r = i / (16 / N), o = i % (16 / N) * N;
-    const bool valid = row0 + r < nrows && at + o < per_row;
-    const uint8_t* from = valid ? src + (row0 + r) * per_row + at + o : src;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(slot + r * 16 + o)),
-                 "l"(from), "n"(N), "r"(valid ? N : 0)
-                 : "memory");
+  const int rows = (int)min((long long)ROWS, nrows - row0);
+  const int bytes = per_row - at;
+  const uint8_t* s = src + (row0 + lane) * per_row + at;
+  uint32_t to = smem_u32(slot + lane * 16);
+#pragma unroll
+  for (int r = 0; r < ROWS; r += 32) {
+    const bool valid = r + lane < rows;
+    if (ROWS >= 32 || lane < ROWS) {
+#pragma unroll
+      for (int o = 0; o < 16; o += N) {
+        const bool some = valid && o < bytes;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to + o),
+                     "l"(some ? s + o : src), "n"(N), "r"(some ? N : 0)
+                     : "memory");
+      }
+    }
+    s += 32 * per_row;
+    to += 32 * 16;
   }
   cp_async_arrive_noinc(raw);
 }
@@ -367,22 +377,26 @@ template <int ROWS>
 LORA_DEV void copy_scale_words(uint8_t* slot, const uint8_t* src, const uint8_t* end, long long row0,
                                long long nrows, int per_row, int at, uint64_t* raw) {
   const int lane = threadIdx.x & 31;
+  const int rows = (int)min((long long)ROWS, nrows - row0);
+  const uint8_t* s = src + (row0 + lane) * per_row + at;
+  uint32_t to = smem_u32(slot + lane * 20);
 #pragma unroll
-  for (int j = 0; j < (ROWS + 31) / 32; ++j) {
-    const int r = j * 32 + lane;
-    if (r < ROWS) {
-      const uint8_t* s = src + (row0 + r) * per_row + at;
+  for (int r = 0; r < ROWS; r += 32) {
+    const bool valid = r + lane < rows;
+    if (ROWS >= 32 || lane < ROWS) {
       const uint8_t* first = s - (reinterpret_cast<uintptr_t>(s) & 3u);
-      const long long left = row0 + r < nrows ? end - first : 0;
-      const uint32_t to = smem_u32(slot + r * 20);
+      const bool inside = valid && end - first >= 20;
 #pragma unroll
       for (int o = 0; o < 20; o += 4) {
-        const int n = (int)max(0LL, min(4LL, left - o));
+        int n = inside ? 4 : 0;
+        if (valid && !inside) n = (int)max(0LL, min(4LL, (long long)(end - first) - o));
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + o),
                      "l"(n > 0 ? first + o : src), "r"(n)
                      : "memory");
       }
     }
+    s += 32 * per_row;
+    to += 32 * 20;
   }
   cp_async_arrive_noinc(raw);
 }
