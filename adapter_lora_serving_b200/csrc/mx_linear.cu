@@ -59,13 +59,17 @@ constexpr int kBlockK = 512;          // elements of k per block of scales (16 b
 constexpr int kSfAtom = 512;          // scales of 128 rows x 128 elements
 constexpr int kTurn = 1024;            // an epilogue warp's 16 rows x 32 features of 16 bits
 constexpr int kHeader = 6144;         // barriers, scan scratch and the experts' tile prefix (1025 ints)
+constexpr int kOffsets = 4608;        // a copy of the experts' offsets (1025 ints)
 
 template <int BN>
 struct Cfg {
   static constexpr int kBTile = BN * kK / 2;
   static constexpr int kStage = kATile + kBTile;
   static constexpr int kStages = BN >= 256 ? 4 : BN >= 128 ? 6 : BN >= 64 ? 8 : BN >= 32 ? 9 : 8;
-  static constexpr int kSfSlots = BN >= 256 ? 3 : BN >= 64 ? 4 : 5;   // blocks of scales in flight
+  static constexpr int kSfSlots = BN >= 64 ? 3 : 5;   // blocks of scales in flight
+  // the experts' offsets in shared memory, where there is room: a tile is looked up
+  // by every role, from global memory in about a thousand cycles
+  static constexpr bool kOwnOffsets = BN <= 128;
   static constexpr int kAtoms = BN > 128 ? 2 : 1;             // of x, per 128 elements of k
   // a slot: raw rows of 16 bytes, or (up to 128 rows) of the 20 around 16 unaligned
   // ones, W's then X's; put in order in place
@@ -79,7 +83,7 @@ struct Cfg {
   static constexpr int kWarpCols = BN >= 64 ? BN / 2 : 32;    // columns an epilogue warp drains
   static constexpr int kThreads = 160 + 32 * kEpiWarps;       // and the scales' producer
   static constexpr int kSmem = 1024 + kHeader + kStages * kStage + kSfSlots * kSfSlot +
-                               kEpiWarps * kTurn;   // 1024: alignment slack
+                               kEpiWarps * kTurn + (kOwnOffsets ? kOffsets : 0);   // 1024: alignment slack
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -234,7 +238,7 @@ struct Plan {
 
 // Tiles of BN rows before each expert (the whole CTA; __syncthreads follows).
 template <int BN, int THREADS>
-LORA_DEV Plan make_plan(const Params& p, int* prefix, int* scratch) {
+LORA_DEV Plan make_plan(const Params& p, int* prefix, int* scratch, int* own_offsets = nullptr) {
   Plan plan = {prefix, p.q.expert_offsets, 0};
   if (plan.offsets == nullptr) {
     plan.tiles = ((p.q.rows + BN - 1) / BN) * p.ftiles;
@@ -247,6 +251,10 @@ LORA_DEV Plan make_plan(const Params& p, int* prefix, int* scratch) {
     int cnt = 0;
     if (e < p.q.experts) {
       const int lo = plan.offsets[e], hi = plan.offsets[e + 1];
+      if (own_offsets != nullptr) {
+        own_offsets[e] = lo;
+        if (e + 1 == p.q.experts) own_offsets[e + 1] = hi;
+      }
       if (lo < 0 || hi > p.q.rows || hi < lo) bad |= LORA_FLAG_BAD_OFFSETS;
       else cnt = (hi - lo + BN - 1) / BN * p.ftiles;
     }
@@ -273,6 +281,7 @@ LORA_DEV Plan make_plan(const Params& p, int* prefix, int* scratch) {
     plan.tiles = prefix[p.q.experts];
   }
   if (blockIdx.x == 0) raise_flag(p.q.flags, bad);
+  if (own_offsets != nullptr) plan.offsets = own_offsets;   // (after the barriers above)
   return plan;
 }
 
@@ -287,7 +296,7 @@ LORA_DEV Tile tile_of(const Params& p, const Plan& plan, int u) {
     u -= plan.prefix[e];
   }
   const int rt = (hi - lo + BN - 1) / BN;   // row tiles run fastest: they share the weight tile
-  const int f = u / rt;
+  const int f = rt == 1 ? u : u / rt;
   t.row0 = lo + (u - f * rt) * BN;
   t.rows = min(BN, hi - t.row0);
   t.f0 = f * FEATURES;
@@ -563,7 +572,9 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     tmem_alloc(tmem_slot, C::kCols);
     tmem_relinquish();
   }
-  const Plan plan = make_plan<BN, C::kThreads>(p, prefix, scratch);
+  const Plan plan = make_plan<BN, C::kThreads>(
+      p, prefix, scratch,
+      C::kOwnOffsets ? reinterpret_cast<int*>(turn + C::kEpiWarps * kTurn) : nullptr);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
