@@ -206,12 +206,14 @@ def _route(x, bias, k, score="softmax", G=1, g=1, pair=False, renorm=True, scale
     return ids, w, int(flags.item())
 
 
-def _check_route(x, bias, k, **kw):
-    ids, w, flags = _route(x, bias, k, **kw)
+def _check_route(x, bias, k, repeat=1, **kw):
+    """repeat: the rows that many times over (the oracle sees them once)."""
+    ids, w, flags = _route(x.repeat(repeat, 1), bias, k, **kw)
     xh = _host(x)
     ref_ids, ref_w, ref_flags = O.route(
         xh, None if bias is None else _host(bias), k, kw.get("score", "softmax"), kw.get("G", 1),
         kw.get("g", 1), kw.get("pair", False), kw.get("renorm", True), kw.get("scale", 1.0))
+    ref_ids, ref_w = np.tile(ref_ids, (repeat, 1)), np.tile(ref_w, (repeat, 1))
     assert (ids.cpu().numpy() == ref_ids).all(), np.argwhere(ids.cpu().numpy() != ref_ids)[:4]
     fin = np.where(np.isfinite(xh), np.abs(xh), 0)
     tol = (4 * fin.max() + x.shape[1] / 32 + 16) * U * np.abs(ref_w) + 2.0 ** -126
@@ -248,7 +250,10 @@ def test_route_groups(score, pair, E, G, g, k):
     ("bf16", "sigmoid", 256, 8, dict(G=8, g=4, pair=True)), ("bf16", "softmax", 128, 6, dict()),
     ("f32", "sigmoid", 160, 15, dict(renorm=False)), ("f16", "softmax", 72, 3, dict(scale=2.5)),
     ("bf16", "softmax", 200, 4, dict(renorm=False)), ("f32", "softmax", 128, 8, dict(G=16, g=5)),
-    ("bf16", "sigmoid", 128, 8, dict(G=4, g=2, pair=True, renorm=False))])
+    ("bf16", "sigmoid", 128, 8, dict(G=4, g=2, pair=True, renorm=False)),
+    ("bf16", "softmax", 8, 2, dict()), ("f32", "sigmoid", 8, 3, dict(renorm=False)),
+    ("f16", "softmax", 16, 12, dict(renorm=False)), ("bf16", "sigmoid", 27, 4, dict(scale=2.5)),
+    ("f32", "softmax", 32, 6, dict())])
 def test_route_many_tokens(name, score, E, k, kw):
     """Several tokens a warp: masked and padded tokens, ties and close calls among
     the rest."""
@@ -266,10 +271,11 @@ def test_route_many_tokens(name, score, E, k, kw):
         s = 1 / (1 + np.exp(-row)) if score == "sigmoid" else np.exp(row - row.max()) / np.exp(row - row.max()).sum()
         close = bias.copy()
         close[::2] = (0.5 - s)[::2]                 # (every other expert's)
-    _check_route(x, _dev(bias, t.float32), k, score=score, **kw)
-    _check_route(x, _dev(close, t.float32), k, score=score, **kw)
+    _check_route(x, _dev(bias, t.float32), k, score=score, repeat=4 if E <= 32 else 1, **kw)
+    _check_route(x, _dev(close, t.float32), k, score=score, repeat=4 if E <= 32 else 1, **kw)
+    _check_route(x, None, k, score=score, repeat=4 if E <= 32 else 1, **kw)
     x[11, 5], x[4000, 0] = float("nan"), float("inf")
-    _check_route(x, _dev(bias, t.float32), k, score=score, **kw)
+    _check_route(x, _dev(bias, t.float32), k, score=score, repeat=4 if E <= 32 else 1, **kw)
 
 
 def test_route_ties_go_to_the_lowest_index():
@@ -361,7 +367,7 @@ def _group(ids, slot, E):
 
 
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 128), (37, 8, 128), (700, 3, 60), (2048, 8, 64),
-                                   (513, 8, 1024), (5000, 2, 8), (9000, 4, 256)])
+                                   (513, 8, 1024), (5000, 2, 8), (9000, 4, 256), (20011, 4, 1024)])
 def test_group(T, k, E):
     rng = np.random.default_rng(T + k + E)
     ids = np.stack([rng.permutation(E)[:k] for _ in range(T)])
