@@ -105,15 +105,17 @@ LORA_DEV uint32_t up1024(uint32_t v) { return (v + 1023u) & ~1023u; }
 // Phase test with a long suspension of the waiting thread (20 us at most; a dozen
 // warps wait most of the time, and their polling costs power, that is clock: 34.7
 // us against 34.1 for 32 x 8 rows of 128 experts).  CLUSTER: for arrivals of
-// another CTA, which it acquires.
+// another CTA, with what its shared memory held before them (the fence is for shared
+// memory alone: an acquire at cluster scope drops the L1 cache with every wait).
 template <bool CLUSTER>
 LORA_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   if (CLUSTER)
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
+        "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "fence.acquire.sync_restrict::shared::cluster.cluster;\n\t}"
         : "=r"(ok)
         : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
         : "memory");
@@ -150,12 +152,14 @@ LORA_DEV bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, u
 
 // The same barrier of the cluster's first CTA, and an arrival there.
 LORA_DEV uint32_t at_first(const uint64_t* bar) { return dsmem_addr(bar, 0); }
-// (Release at the default scope: what the arrivals follow is ordered for the tensor
-// core by a proxy fence or a tcgen05 fence already, and a release at cluster scope
-// made the pair kernel's stages a third longer: 470 us for 8192 x 4096 x 28672, 351
-// without.)
+// For what this CTA's warp wrote to its shared memory (RELEASE), or for accesses to
+// tensor memory, which the tcgen05 fences around an arrival and its wait order.  The
+// release is for shared memory alone: one of all memory takes over a microsecond, 488
+// us for 8192 x 4096 x 28672 with one for every block of scales, 361 as here.
+template <bool RELEASE>
 LORA_DEV void arrive_at_first(const uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(at_first(bar))
+  if (RELEASE) asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(at_first(bar))
                : "memory");
 }
 // A ring position and the parity of its current round.
@@ -344,7 +348,7 @@ LORA_DEV void order_scales(uint8_t* ring, int slot_bytes, uint64_t* raw, uint64_
     __syncwarp();
     write_ordered<ATOMS>(slot, v);
     if (lane == 0) {
-      if (PAIR) arrive_at_first(&ready[b.s]);
+      if (PAIR) arrive_at_first<true>(&ready[b.s]);
       else mbar_arrive(&ready[b.s]);
     }
     b.next<SLOTS>();
@@ -977,7 +981,7 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
         // the MMAs' columns are split between the CTAs
         const int x_row = t.row0 + rank * (columns_of(t, ROWS) / 2);
         for (int k = 0; k < stages; ++k) {
-          if (!wait_or_stop(&empty[r.s], r.round ^ 1u, stop, p.q.flags)) break;
+          if (!wait_or_stop<true>(&empty[r.s], r.round ^ 1u, stop, p.q.flags)) break;
           uint8_t* slot = ring + r.s * C::kStage;
           const uint32_t bar = at_first(&full[r.s]);
           if (rank == 0) mbar_arrive_expect_tx(&full[r.s], 2 * C::kStage);
@@ -1019,7 +1023,7 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
             commit_pair(&sf_empty[b.s]);
             b.next<kSl>();
           }
-          if (!(ok = wait_or_stop(&full[r.s], r.round, stop, p.q.flags))) break;
+          if (!(ok = wait_or_stop<true>(&full[r.s], r.round, stop, p.q.flags))) break;
           tc_fence_after();
           const uint32_t a_lo = ring_lo + (uint32_t)r.s * (C::kStage >> 4);
           const uint32_t b_lo = a_lo + (kATile >> 4);
@@ -1049,7 +1053,7 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
       for (int i = 0; i < units && ok; ++i) {
         const Tile t = unit(i);
         for (int k = 0; k < blocks; ++k) {
-          if (!(ok = wait_or_stop(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags))) break;
+          if (!(ok = wait_or_stop<true>(&sf_empty[b.s], b.round ^ 1u, stop, p.q.flags))) break;
           uint8_t* slot = sf_ring + b.s * C::kSfSlot;
           mbar_arrive_expect_tx(&sf_raw[b.s], kM * 16);
           tma_load_2d(slot, &map_ws, k * (kBlockK / 32), t.wrow, &sf_raw[b.s]);
@@ -1066,7 +1070,7 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
     Ring acc;
     for (int i = 0; i < units; ++i, acc.next<C::kAcc>()) {
       const Tile t = unit(i);
-      if (!wait_or_stop(&accfull[acc.s], acc.round, stop, p.q.flags)) break;
+      if (!wait_or_stop<true>(&accfull[acc.s], acc.round, stop, p.q.flags)) break;
       __syncwarp();
       tc_fence_after();
       const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc.s * ROWS + c_first);
@@ -1082,7 +1086,7 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
           }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at_first(&accempty[acc.s]);
+        if (lane == 0) arrive_at_first<false>(&accempty[acc.s]);
 #pragma unroll
         for (int c = 0; c < kParts; ++c) {
           const int c0 = c_first + c * 32;
@@ -1107,7 +1111,7 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_at_first(&accempty[acc.s]);
+        if (lane == 0) arrive_at_first<false>(&accempty[acc.s]);
       }
     }
   }

@@ -1,6 +1,7 @@
 """The routed layer's entry points on a host without a GPU: refusals before any
 launch (C ABI and binding), and hand-derived pins of their fp64 oracle."""
 import os
+import re
 
 import numpy as np
 import pytest
@@ -201,3 +202,39 @@ def test_oracle_combine_by_hand():
     out, _, flags = O.combine(y, np.array([[1, 0], [-1, 1], [0, 5]]),
                               np.array([[0.5, 2.0], [9.0, 0.1], [1.0, 1.0]]), np.ones((3, 2)))
     assert np.allclose(out, [[8.0, 15.0], [2.0, 3.0], [2.0, 3.0]]) and flags == O.FLAG_BAD_ROW
+
+
+# ---------------------------------------------------------------------------
+# ordering between the CTAs of a cluster
+# ---------------------------------------------------------------------------
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                    "adapter_lora_serving_b200", "csrc")
+
+
+def _csrc():
+    for name in sorted(os.listdir(CSRC)):
+        yield name, open(os.path.join(CSRC, name)).read()
+
+
+def test_arrivals_at_another_cta_have_cluster_scope():
+    """An arrival without a scope orders the arriving CTA's accesses for that CTA
+    alone, whatever the waiting side acquires."""
+    found = 0
+    for name, text in _csrc():
+        for op in re.findall(r'"(mbarrier\.arrive[a-z_.:]*shared::cluster[a-z0-9_.:]*)', text):
+            found += 1
+            assert re.search(r"\.(release|relaxed)\.cluster\.", op), f"{name}: {op}"
+    assert found
+
+
+def test_scales_of_the_second_cta_are_released():
+    """The reordered scales are plain stores to shared memory, which the tensor core
+    reads on the other CTA's request: the arrival that announces them releases them
+    at cluster scope, and every wait of that kernel acquires there."""
+    text = dict(_csrc())["mx_linear.cu"]
+    release = 'if (RELEASE) asm volatile("fence.release.sync_restrict::shared::cta.cluster;"'
+    assert release in text and "if (PAIR) arrive_at_first<true>(&ready[b.s]);" in text
+    assert "fence.acquire.sync_restrict::shared::cluster.cluster;" in text
+    pair = text[text.index("mx_linear_pair_kernel(const __grid_constant__"):]
+    assert "wait_or_stop<true>(" in pair and "wait_or_stop(" not in pair
