@@ -150,6 +150,13 @@ LORA_DEV bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, u
   return true;
 }
 
+// The same for a whole warp, whose lanes go on or give up together: collective
+// instructions follow, and one lane can see its time run out when another does not.
+template <bool CLUSTER = false>
+LORA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* stop, uint32_t* flags) {
+  return __all_sync(0xffffffffu, wait_or_stop<CLUSTER>(bar, parity, stop, flags));
+}
+
 // The same barrier of the cluster's first CTA, and an arrival there.
 LORA_DEV uint32_t at_first(const uint64_t* bar) { return dsmem_addr(bar, 0); }
 // For what this CTA's warp wrote to its shared memory (RELEASE), or for accesses to
@@ -338,7 +345,7 @@ LORA_DEV void order_scales(uint8_t* ring, int slot_bytes, uint64_t* raw, uint64_
   Ring b;
   for (int n = 0; n < total; ++n) {
     uint8_t* slot = ring + b.s * slot_bytes;
-    if (!wait_or_stop(&raw[b.s], b.round, stop, flags)) break;
+    if (!warp_wait(&raw[b.s], b.round, stop, flags)) break;
     uint4 v[ATOMS][4];
 #pragma unroll
     for (int h = 0; h < ATOMS; ++h)
@@ -428,7 +435,7 @@ LORA_DEV void order_scale_words(uint8_t* ring, int slot_bytes, uint64_t* raw, ui
     for (int k = 0; k < blocks; ++k) {
       const int at = (block0 + k) * (kBlockK / 32);
       uint8_t* slot = ring + b.s * slot_bytes;
-      if (!(ok = wait_or_stop(&raw[b.s], b.round, stop, flags))) break;
+      if (!(ok = warp_wait(&raw[b.s], b.round, stop, flags))) break;
       uint4 v[1][4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -728,7 +735,7 @@ mx_linear_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constan
     Ring acc;
     for (int i = 0; i < units; ++i) {
       const Tile t = tile_of<BN>(p, plan, first_unit + i * unit_step);
-      if (!wait_or_stop(&accfull[acc.s], acc.round, stop, p.q.flags)) break;
+      if (!warp_wait(&accfull[acc.s], acc.round, stop, p.q.flags)) break;
       __syncwarp();
       tc_fence_after();
       const int f = t.f0 + quarter * 32 + lane;
@@ -1070,7 +1077,7 @@ mx_linear_pair_kernel(const __grid_constant__ CUtensorMap map_w,
     Ring acc;
     for (int i = 0; i < units; ++i, acc.next<C::kAcc>()) {
       const Tile t = unit(i);
-      if (!wait_or_stop<true>(&accfull[acc.s], acc.round, stop, p.q.flags)) break;
+      if (!warp_wait<true>(&accfull[acc.s], acc.round, stop, p.q.flags)) break;
       __syncwarp();
       tc_fence_after();
       const uint32_t src = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc.s * ROWS + c_first);

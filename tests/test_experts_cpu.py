@@ -238,3 +238,12 @@ def test_scales_of_the_second_cta_are_released():
     assert "fence.acquire.sync_restrict::shared::cluster.cluster;" in text
     pair = text[text.index("mx_linear_pair_kernel(const __grid_constant__"):]
     assert "wait_or_stop<true>(" in pair and "wait_or_stop(" not in pair
+
+
+def test_warps_give_up_together():
+    """A bounded wait ahead of warp-wide instructions ends alike in all lanes: those
+    of the warps that reorder scales and that drain the accumulator."""
+    text = dict(_csrc())["mx_linear.cu"]
+    waits = re.findall(r"(\w+)(?:<true>)?\((&raw\[b\.s\]|&accfull\[acc\.s\]), ", text)
+    assert len(waits) == 4 and {w for w, _ in waits} == {"warp_wait"}
+    assert "__all_sync(0xffffffffu, wait_or_stop" in text
