@@ -76,6 +76,14 @@ class MoeLayer:
         self.bias = routing.pop("bias", None)
         self.routing = routing
         self.device = gate_up[0].device
+        for ad, slices, n_in, out in ((gate_up_adapters, 2, hidden, 2 * inter),
+                                      (down_adapters, 1, inter, hidden)):
+            if ad is not None:
+                self._check_adapters(ad, "expert", ad.num_pairs * slices * ad.R * n_in,
+                                     ad.num_pairs * out * ad.R, ad.slots * num_experts)
+        if router_adapters is not None:
+            n = router_adapters.slots * router_adapters.R
+            self._check_adapters(router_adapters, "router", n * hidden, n * num_experts, 0)
         rows = max_tokens * top_k
 
         def empty(dtype, *shape):
@@ -107,10 +115,50 @@ class MoeLayer:
         self.router_ws = (torch.zeros(self.router_bytes, dtype=u8, device=self.device)
                           if self.router_bytes else None)
 
+    def _check_adapters(self, ad, what, of_a, of_b, of_index):
+        """The folds' entry points take addresses: what stands behind these is looked
+        at here, once."""
+        import torch
+        bf16 = torch.bfloat16
+        for name, dtype, n in (("a", bf16, of_a), ("b", bf16, of_b),
+                               ("ranks", torch.int32, ad.slots),
+                               ("scalings", torch.float32, ad.slots),
+                               ("pair_index", torch.int32, of_index)):
+            t = getattr(ad, name, None)
+            if t is None or t.__class__ is int:
+                continue
+            if t.dtype is not dtype or not t.is_contiguous() or t.numel() < n or t.device != self.device:
+                raise ValueError(f"{name} of the {what} adapters: {t.dtype} {tuple(t.shape)} on "
+                                 f"{t.device}, not {n} contiguous {dtype} on {self.device}")
+
+    def _check_inputs(self, T, x, gate_logits, out, token_slot, token_order, slot_indptr,
+                      residual, flags):
+        """Every argument, before the first kernel: the router fold, which runs first,
+        takes addresses."""
+        op, E = "MoeLayer.forward", self.num_experts
+        if x.numel() != T * self.hidden:
+            L._refuse(op, f"x has {x.numel() // T} features a token, the layer {self.hidden}")
+        for name, t, n in (("gate_logits", gate_logits, E), ("out", out, self.hidden),
+                           ("residual", residual, self.hidden)):
+            if t is not None and t.__class__ is not int and t.dim() > 1 and t.shape[-1] != n:
+                L._refuse(op, f"{name} has rows of {t.shape[-1]}, not of {n}")
+        bf16, i32, rt = L.LORA_TYPE_BF16, "int32", self.router_adapters
+        of_logits = bf16
+        if rt is None:   # the routing takes logits of any LORA_TYPE_*
+            of_logits = L._type_of(op, "gate_logits", gate_logits, None)
+            token_order = slot_indptr = None
+        n = T * self.hidden
+        L._pointers(op, (x, gate_logits, out, residual, token_slot, token_order, slot_indptr, flags),
+                    (bf16, of_logits, bf16, bf16, i32, i32, i32, i32),
+                    (n, T * E, n, n, T, 0, rt.slots + 1 if rt is not None else 0, 1),
+                    ("x", "gate_logits", "out", "residual", "token_slot", "token_order",
+                     "slot_indptr", "err_flags"))
+
     def forward(self, x, gate_logits, out, token_slot=None, token_order=None, slot_indptr=None,
                 residual=None, err_flags=None, stream=None):
         """out [T, hidden] = residual + the layer of x [T, hidden] (bf16) routed by
-        gate_logits [T, num_experts] (bf16; the router delta is added in place).
+        gate_logits [T, num_experts] (bf16, and the router delta is added in place;
+        without router adapters fp16 or fp32 too).
         token_slot [T] int32 (-1 = no adapter) is needed with expert adapters;
         token_order and slot_indptr (CSR by slot) with router adapters."""
         import torch
@@ -125,6 +173,8 @@ class MoeLayer:
             raise ValueError("router adapters need token_order and slot_indptr")
         if T == 0:
             return out
+        self._check_inputs(T, x, gate_logits, out, token_slot, token_order, slot_indptr, residual,
+                           err_flags)
         with torch.cuda.device(self.device):
             self._forward(x, gate_logits, out, T, k, E, token_slot, token_order, slot_indptr,
                           residual, err_flags, stream)

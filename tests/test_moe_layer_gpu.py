@@ -241,3 +241,40 @@ def test_layer_refusals():
             c.x, t.zeros(16, 8, dtype=t.bfloat16, device="cuda").t(), out)
     with pytest.raises(L.LoraError, match="element"):
         L.lora_mx_dequantize(c.layer.x_codes, c.layer.x_scales, out, c.T + 1, c.hidden)
+
+
+def test_layer_with_router_refuses_before_the_fold():
+    """With router adapters nothing is written when an input is not as the fold, which
+    takes addresses, reads it."""
+    t = _torch()
+    c = Case(T=8)
+    logits, out = c.fresh()
+    kept = logits.clone()
+    wide = t.zeros(8, 2 * c.hidden, dtype=t.bfloat16, device="cuda")
+
+    def call(match, x=c.x, lg=logits, o=out, order=c.order, residual=c.residual):
+        with pytest.raises(L.LoraError, match=match):
+            c.layer.forward(x, lg, o, c.slot, order, c.indptr, residual, c.flags)
+        assert t.equal(logits, kept) and (out == 7.0).all()
+
+    call("element type", lg=logits.float())
+    call("element type", x=c.x.half())
+    call("contiguous", lg=t.zeros(c.E, 8, dtype=t.bfloat16, device="cuda").t())
+    call("contiguous", x=wide[:, :c.hidden])
+    call("contiguous", x=c.x[:1].expand(8, c.hidden))
+    call("features", x=wide)
+    call("features", x=c.x[:, :32].contiguous())
+    call("rows of", lg=t.zeros(8, 2 * c.E, dtype=t.bfloat16, device="cuda"))
+    call("contiguous", o=wide[:, :c.hidden])
+    call("fewer", residual=c.residual[:4])
+    call("element type", order=c.order.long())
+    call("not on a CUDA device", order=c.order.cpu())
+    c.run(logits, out)
+    assert not (out == 7.0).all() and int(c.flags.item()) == 0
+
+
+@pytest.mark.parametrize("name", ["float32", "float16"])
+def test_layer_takes_other_logits_without_a_router_fold(name):
+    c = Case(T=20, router=False)
+    c.logits = c.logits.to(getattr(_torch(), name))
+    _check_steps(c)
