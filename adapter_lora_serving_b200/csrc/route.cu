@@ -226,7 +226,9 @@ LORA_DEV uint32_t best_groups(const RouteParams& p, int lane, U score, uint32_t 
     const U worst_kept = ~warp_max(kept && is_open(score) ? (U)~score : (U)0);
     const U best_out = warp_max(real && !kept ? score : (U)0);
     const float border = tol.of_sum(magnitude);
-    *close |= is_open(best_out) && value_of(worst_kept) - value_of(best_out) <= border;
+    // (keys of 2^127 and more, whose sums fp32 cannot hold, show in the border)
+    *close |= border >= 0x1p109f ||
+              (is_open(best_out) && value_of(worst_kept) - value_of(best_out) <= border);
   }
   return keep;
 }

@@ -634,3 +634,18 @@ def test_products_of_two_streams_at_once():
     for out, (_, w) in zip(outs, calls):
         assert all(t.equal(o, w) for o in out)
     assert int(flags.item()) == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G", [(64, 8), (256, 8), (96, 3), (512, 32)])
+def test_route_pair_sums_past_fp32(score, E, G):
+    """Biases whose pairwise sums leave fp32's range, up or down: the groups are still
+    ranked by those sums, and a group whose sum is below the range can be chosen."""
+    t = _torch()
+    rng = np.random.default_rng(E + G)
+    x = _dev(rng.standard_normal((9, E)), t.float32)
+    far = 2.0e38 + 1e35 * rng.permutation(E)
+    mixed = np.where(np.arange(E) % 3 == 0, 1.0, -1.0) * far
+    for bias in (far, -far, mixed, np.where(np.arange(E) < E // G, far, 0.01 * np.arange(E))):
+        for g in (1, 2):
+            _check_route(x, _dev(bias, t.float32), 4, score=score, G=G, g=g, pair=True)
