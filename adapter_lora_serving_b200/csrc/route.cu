@@ -122,6 +122,18 @@ LORA_DEV void load_bias(const RouteParams& p, int lane, float (&bias)[VPL], bool
   }
 }
 
+// Whether all experts have one bias, a finite one (VPL of them in each lane, e0 the
+// lane's first; the caller votes): then the order of the keys is that of the logits,
+// also where scores are equal in 64 bits.
+template <int VPL>
+LORA_DEV bool one_bias(const RouteParams& p, const float (&bias)[VPL], int e0) {
+  const float first = __ldg(p.bias);
+  bool same = fabsf(first) < INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) same = same && (e0 + i >= p.E || bias[i] == first);
+  return same;
+}
+
 // e^z and 1 / a: in 64 bits, or for fp32 keys whose error is accounted for (Within)
 // the fast ones: 2 + 1.173 |z| ulps and 2 ulps.
 LORA_DEV double power(double z) { return exp(z); }
@@ -559,24 +571,26 @@ __device__ __noinline__ int select_in_double(const RouteParams& p, const LT* row
                                                Exact(), &close, NoKey());
 }
 
-// One warp per token.  Without a bias (and without pair scores of groups) the
-// order of the scores is the order of the logits, so the logits themselves are
-// the keys and the choice is exact.  Else the keys are fp32 scores plus bias;
-// where two that decide the outcome lie within their error bound they are
-// compared in 64 bits (the filter), so that the chosen experts are those of exact
-// arithmetic.  Bound by its instructions (about 950 a token with groups and a bias;
+// One warp per token.  Without a bias, or with one for all (and without pair scores of
+// groups), the order of the scores is the order of the logits, so the logits
+// themselves are the keys and the choice is exact.  Else the keys are fp32 scores plus
+// bias; where two that decide the outcome lie within their error bound they are
+// compared in 64 bits (the filter), so that the chosen experts are those of keys in
+// 64 bits.  Bound by its instructions (about 950 a token with groups and a bias;
 // 16384 tokens of 256 experts: 23.5 us, of which the rounds 6, the groups 5 and the
 // close calls 1.3; without groups and bias, 2048 of 128: 2.7 us).
 template <int VPL, typename LT>
 __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_kernel(const __grid_constant__ RouteParams p) {
   const int lane = threadIdx.x & 31;
   const int warps = (int)(blockDim.x >> 5);
-  const bool by_score =
-      p.bias != nullptr || (p.num_groups > 1 && p.group_score == LORA_GROUP_TOP_PAIR);
+  bool by_score = p.bias != nullptr || (p.num_groups > 1 && p.group_score == LORA_GROUP_TOP_PAIR);
   const int span = group_span<VPL>(p);
   bool bad = false;
   float bias[VPL];
   if (by_score) load_bias<VPL>(p, lane, bias, &bad);
+  if (p.bias != nullptr && (p.num_groups == 1 || p.group_score == LORA_GROUP_MAX) &&
+      __all_sync(0xffffffffu, one_bias<VPL>(p, bias, lane * VPL)))
+    by_score = false;
   for (long long t = (long long)blockIdx.x * warps + (threadIdx.x >> 5); t < p.T;
        t += (long long)gridDim.x * warps) {
     const LT* row = reinterpret_cast<const LT*>(p.logits) + (size_t)t * p.E;
@@ -741,8 +755,16 @@ __device__ __noinline__ uint64_t choose_in_thread_double(const RouteParams& p, c
   double s[EM];
   bool bad = false, close = false;
   load_in_thread<EM, LT>(row, p.E, x, &bad);
-  scores_in_thread<EM, double>(p, x, s);
-  keys_in_thread<EM, double>(p, x, s, &bad);
+  float bias[EM];
+#pragma unroll
+  for (int i = 0; i < EM; ++i) bias[i] = i < p.E ? __ldg(p.bias + i) : 0.0f;
+  if (one_bias<EM>(p, bias, 0)) {
+#pragma unroll
+    for (int i = 0; i < EM; ++i) s[i] = (double)x[i];
+  } else {
+    scores_in_thread<EM, double>(p, x, s);
+    keys_in_thread<EM, double>(p, x, s, &bad);
+  }
   return choose_in_thread<EM, double>(p.top_k, s, Exact(), count, &close);
 }
 

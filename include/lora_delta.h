@@ -309,10 +309,13 @@ LORA_API lora_status lora_expert_apply(const void* x_sorted, void* y_sorted, con
  * With num_groups > 1 the experts fall into num_groups equal consecutive groups;
  * only those of the best top_groups groups (by group_score of their keys) can be
  * chosen.  topk_ids[t] are the top_k experts of the largest keys, in descending
- * order; every tie goes to the lowest index.
+ * order.  Without a bias, or with one that is the same finite number for all experts,
+ * and without LORA_GROUP_TOP_PAIR the logits themselves are compared (the scores have
+ * their order); else keys, and sums of two, as computed in 64 bits.  Every tie, also
+ * one that 64 bits make (scores that saturate, underflow or vanish beside a bias),
+ * goes to the lowest index.
  *   topk_weights[t, j] = s[t, id_j] (/ sum over the chosen, if renormalize) * scale
- * The bias takes part in the choice alone.  The choice is that of exact
- * arithmetic on the given logits and bias; the weights are computed in fp32.
+ * The bias takes part in the choice alone.  The weights are computed in fp32.
  * logits [T, num_experts] of `type`; bias [num_experts] fp32 or NULL; topk_ids
  * [T, top_k] int32; topk_weights [T, top_k] fp32.
  * An expert whose logit or bias is -inf is masked: it is never chosen (a masked

@@ -35,9 +35,10 @@ def route(logits, bias, top_k, score="softmax", num_groups=1, top_groups=1, pair
             with np.errstate(over="ignore"):
                 s = 1.0 / (1.0 + np.exp(-x))
         open_ = (x > -np.inf) & ~b_bad & (b > -np.inf)
-        # without a bias the order of the scores is that of the logits, also
-        # where scores underflow or saturate
-        by_logit = bias is None and not (num_groups > 1 and pair)
+        # without a bias, or with one for all, the order of the scores is that of the
+        # logits, also where scores underflow or saturate
+        one = bias is None or (np.isfinite(b).all() and (b == b[0]).all())
+        by_logit = one and not (num_groups > 1 and pair)
         key = np.where(open_, x if by_logit else s + np.where(open_, b, 0.0), -np.inf)
         if num_groups > 1 and top_groups < num_groups:
             n = E // num_groups

@@ -247,3 +247,13 @@ def test_warps_give_up_together():
     waits = re.findall(r"(\w+)(?:<true>)?\((&raw\[b\.s\]|&accfull\[acc\.s\]), ", text)
     assert len(waits) == 4 and {w for w, _ in waits} == {"warp_wait"}
     assert "__all_sync(0xffffffffu, wait_or_stop" in text
+
+
+def test_oracle_route_saturated_by_hand():
+    """Sigmoids of 50 and 60 are 1 in 64 bits: with one bias for all experts the
+    logits decide, with several the lowest index."""
+    x = [[50.0, 60.0, 0.0, 50.0]]
+    for bias in (None, [0.0] * 4, [2.5] * 4):
+        assert O.route(x, bias, 3, "sigmoid")[0].tolist() == [[1, 0, 3]]
+        assert O.route(x, bias, 3, "sigmoid", 2, 1)[0][0, :2].tolist() == [1, 0]
+    assert O.route(x, [0.0, 0.0, 0.25, 0.0], 3, "sigmoid")[0].tolist() == [[0, 1, 3]]

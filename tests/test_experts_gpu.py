@@ -649,3 +649,46 @@ def test_route_pair_sums_past_fp32(score, E, G):
     for bias in (far, -far, mixed, np.where(np.arange(E) < E // G, far, 0.01 * np.arange(E))):
         for g in (1, 2):
             _check_route(x, _dev(bias, t.float32), 4, score=score, G=G, g=g, pair=True)
+
+
+def _ids(x, bias, k, repeat=1, **kw):
+    t = _torch()
+    b = None if bias is None else _dev(np.asarray(bias, dtype=np.float64), t.float32)
+    ids, _, flags = _route(_dev(np.asarray(x, dtype=np.float64), t.float32).repeat(repeat, 1), b, k, **kw)
+    assert flags == 0
+    return ids.cpu().numpy()
+
+
+@pytest.mark.parametrize("repeat", [1, 8192])      # a warp a token, a thread a token
+def test_route_saturated_scores_by_hand(repeat):
+    """Scores that are equal in 64 bits: sigmoids of 38, 50 and 60 are 1, softmax
+    scores of -800 and -760 beside 0 are 0.  With one bias for all the larger logit
+    has the larger key all the same; with several, equal keys go by the index."""
+    x = [[38.0, 50.0, -1.0, 50.0, 60.0, 0.0, 37.9, 45.0]] * 2
+    want = [[4, 1, 3, 7, 0]] * (2 * repeat)
+    for bias in (None, [0.0] * 8, [0.25] * 8, [1e9] * 8, [-3.0] * 8):
+        assert _ids(x, bias, 5, repeat, score="sigmoid").tolist() == want
+    x = [[-800.0, 0.0, -760.0, -900.0, -760.0, -1.0, -790.0, -2000.0]] * 2
+    want = [[1, 5, 2, 4, 6, 0, 3, 7]] * (2 * repeat)
+    for bias in (None, [0.0] * 8, [0.5] * 8):
+        assert _ids(x, bias, 8, repeat).tolist() == want
+    # keys 1, 1.5, 1.5 - 8e-7 and 1
+    x = [[39.0, 38.0, 14.0, 60.0]] * 2
+    assert _ids(x, [0.0, 0.5, 0.5, 0.0], 4, repeat, score="sigmoid").tolist() == [[1, 2, 0, 3]] * (2 * repeat)
+
+
+@pytest.mark.parametrize("E", [8, 27, 64, 128, 256, 384, 512, 1000])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_one_bias_leaves_the_order_of_the_logits(E, score):
+    """Logits over a range where most scores are equal in 64 bits: with one bias for
+    all experts, small or large, the choice is that without any."""
+    rng = np.random.default_rng(E)
+    t = _torch()
+    x = np.round(rng.uniform(-900, 900, (40, E))) * (1.0 if score == "softmax" else 0.25)
+    x = np.concatenate([x, np.abs(x) + 40.0])
+    for kw in [dict()] + ([dict(G=8, g=3)] if E % 8 == 0 and E > 8 else []):
+        k = min(8, E)
+        want = _ids(x, None, k, score=score, **kw)
+        for bias in (0.0, 0.375, -7.0, 1e12):
+            assert (_ids(x, np.full(E, bias), k, score=score, **kw) == want).all()
+        _check_route(_dev(x, t.float32), _dev(np.full(E, 0.375), t.float32), k, score=score, **kw)
