@@ -198,10 +198,16 @@ struct Exact {
 };
 // Twice the error of an fp32 key, in units of u = 2^-23.
 //   sigmoid: e^-x moves the score by s (1 - s) (2 + 1.173 |x|) u < u (|x| s (1 - s)
-//     < .23); the sum and the quotient by 3 s u: 4 u in all.
-//   softmax: a term e^z by s (2 + 1.173 |z|) u <= 2.5 u smax (z e^z < .37); the
-//     sum by 2.5 u and half a u for each of VPL + 5 additions, the quotient and the
-//     product by 2.5 u more: (8 + (VPL + 5) / 2) u smax.
+//     < .23); the sum and the quotient by 3 s u: 4 u in all, 8 for two.
+//   softmax: a term e^z is off by (2 + 1.173 |z|) u, and by half a |z| u for the
+//     rounding of z: e^z (2 + 1.68 |z|) u <= 2 u, and half a u for the product with
+//     the inverse.  The sum is off by the mean of (2 + 1.68 |z|) u over its terms, half
+//     a u for each of VPL + 4 additions and 2 u for the quotient.  That mean is largest
+//     with one expert at 0 and the others at one -w (w = 5.4 of 1024 experts): 5.1,
+//     5.9, 6.8, 7.7, 8.6 and 9.5 for 32, 64 ... 1024 experts.  It is a factor that all
+//     scores share, so it acts on the difference of two, at most smax: counted once.
+//     Two keys: (mean + VPL / 2 + 4 + 5) u smax, at most 35 for VPL = 32 and 15 for 1
+//     (a thread's EM - 1 additions: 28 for 32); here VPL + 22.
 //   the bias sum: half a u of the key; the place within the lane that fills its
 //     three lowest bits (Sorted): 7 u of it.  Two keys: 15 u, here 16.
 // A pair's sum has the errors of both its keys, whose magnitudes its own can be
@@ -217,7 +223,7 @@ struct Within {
 template <int VPL>
 LORA_DEV Within key_error(const RouteParams& p, float smax) {
   Within w;
-  w.of_score = p.score == LORA_SCORE_SIGMOID ? 8.0f * 0x1p-23f : (float)(16 + VPL + 6) * 0x1p-23f * smax;
+  w.of_score = p.score == LORA_SCORE_SIGMOID ? 8.0f * 0x1p-23f : (float)(VPL + 22) * 0x1p-23f * smax;
   return w;
 }
 

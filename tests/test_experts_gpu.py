@@ -692,3 +692,31 @@ def test_route_one_bias_leaves_the_order_of_the_logits(E, score):
         for bias in (0.0, 0.375, -7.0, 1e12):
             assert (_ids(x, np.full(E, bias), k, score=score, **kw) == want).all()
         _check_route(_dev(x, t.float32), _dev(np.full(E, 0.375), t.float32), k, score=score, **kw)
+
+
+@pytest.mark.parametrize("E", [8, 32, 64, 128, 256, 384, 512, 1024])
+def test_route_close_keys_where_the_sum_is_least_exact(E):
+    """One expert at 0 and the others where the mean error of the softmax's terms is
+    largest (z e^z weighted by their number), and biases that leave the keys an odd
+    fraction of an fp32 step to a few steps apart, in an order of their own; with a
+    few of them far below."""
+    t = _torch()
+    rng = np.random.default_rng(E)
+    w = np.linspace(1.0, 8.0, 2000)
+    r = (E - 1) * np.exp(-w)
+    w = w[np.argmax(w * r / (1 + r))]
+    x = np.full((6, E), -w) + rng.uniform(-0.2, 0.2, (6, E))
+    x[:, 0] = 0.0
+    x[3:, E // 2 :] -= 20.0
+    x = x.astype(np.float32).astype(np.float64)
+    s = np.exp(x - x.max(1, keepdims=True))
+    s /= s.sum(1, keepdims=True)
+    k = min(8, E)
+    for row in (0, 1, 3, 5):
+        for step in (0.3, 2.7, 40.0):
+            bias = 0.25 + step * 2.0 ** -25 * rng.permutation(E) - s[row]
+            for repeat in ([1, 2731] if E <= 32 else [1]):
+                _check_route(_dev(x, t.float32), _dev(bias, t.float32), k, repeat=repeat)
+            if E >= 64:
+                _check_route(_dev(x, t.float32), _dev(bias, t.float32), k, G=8, g=3, pair=True)
+                _check_route(_dev(x, t.float32), _dev(bias, t.float32), k, G=8, g=3)
