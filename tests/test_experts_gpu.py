@@ -720,3 +720,36 @@ def test_route_close_keys_where_the_sum_is_least_exact(E):
             if E >= 64:
                 _check_route(_dev(x, t.float32), _dev(bias, t.float32), k, G=8, g=3, pair=True)
                 _check_route(_dev(x, t.float32), _dev(bias, t.float32), k, G=8, g=3)
+
+
+@pytest.mark.parametrize("name,score,E,k,kw", [
+    ("bf16", "sigmoid", 256, 8, dict(G=8, g=4, pair=True)), ("bf16", "softmax", 128, 6, dict()),
+    ("bf16", "softmax", 8, 2, dict()), ("f32", "sigmoid", 8, 3, dict(renorm=False)),
+    ("f16", "softmax", 16, 12, dict(renorm=False)), ("bf16", "sigmoid", 27, 4, dict(scale=2.5)),
+    ("f32", "softmax", 32, 6, dict())])
+def test_route_many_tokens_close_and_masked_biases(name, score, E, k, kw):
+    """Many tokens, and for each of several a bias that brings the keys of every other
+    expert within 2^-25 of one half for it; then biases that mask experts (-inf) and
+    that are NaN or infinite."""
+    t = _torch()
+    rng = np.random.default_rng(E * k)
+    T = 4203 if E <= 32 else 900
+    x = rng.standard_normal((T, E)) * 2
+    x[7, :] = -np.inf
+    x[8, 3:] = -np.inf
+    x[100:200] = np.round(x[100:200])
+    x = _dev(x, _dtype(name))
+    bias = rng.standard_normal(E) * 0.1
+    repeat = 4 if E <= 32 else 1
+    for r in range(300, 900, 100):
+        row = _host(x)[r]
+        e = np.exp(row - row.max())
+        s = 1 / (1 + np.exp(-row)) if score == "sigmoid" else e / e.sum()
+        close = np.where(np.arange(E) % 2 == 0, 0.5 - s, bias)
+        _check_route(x, _dev(close, t.float32), k, score=score, repeat=repeat, **kw)
+    masked = bias.copy()
+    masked[1:E:3] = -np.inf
+    _check_route(x, _dev(masked, t.float32), k, score=score, repeat=repeat, **kw)
+    masked[0], masked[E - 2] = np.nan, np.inf
+    _check_route(x, _dev(masked, t.float32), k, score=score, repeat=repeat, **kw)
+    _check_route(x, _dev(np.full(E, -np.inf), t.float32), k, score=score, repeat=repeat, **kw)
