@@ -268,8 +268,9 @@ lora_status lora_combine_experts(const void* y_sorted, int32_t type, const int32
   TRY(check_count(op, "rows_cap", rows_cap));
   if (top_k <= 0) return fail(LORA_ERR_INVALID, "%s: top_k = %d must be positive", op, top_k);
   TRY(check_multiple(op, "features", features, 8));
-  if (T > (1 << 30) || features > (1 << 26))
-    return fail(LORA_ERR_UNSUPPORTED, "%s: at most 2^30 tokens of 2^26 features", op);
+  // (blocks of 1024 columns are the grid's second dimension)
+  if (T > (1 << 30) || features > 65535 * 1024)
+    return fail(LORA_ERR_UNSUPPORTED, "%s: at most 2^30 tokens of 65535 * 1024 features", op);
   if (T == 0) return ok();
   TRY(check_ptrs(op, {{y_sorted, "y_sorted", 16, rows_cap == 0},
                       {pair_row, "pair_row", 4, false},

@@ -370,7 +370,8 @@ LORA_API lora_status lora_group_experts(const int32_t* topk_ids, const int32_t* 
  * (those past it are left as they were), e.g. &expert_offsets[num_experts].
  * A row_index outside [0, x_rows) skips the row (LORA_FLAG_BAD_ROW).  32 values
  * with a NaN or an infinity among them become scale byte 255 (NaN) and codes 0
- * (LORA_FLAG_NONFINITE).  features % 32 == 0.  rows_out must not overlap x.
+ * (LORA_FLAG_NONFINITE).  features % 32 == 0, features <= 2^24.  rows_out must not
+ * overlap x.
  */
 LORA_API lora_status lora_mx_quantize(const void* x, int32_t type, const int32_t* row_index,
                                       const int32_t* row_count, void* rows_out, uint8_t* codes,
@@ -394,8 +395,9 @@ LORA_API lora_status lora_mx_dequantize(const uint8_t* codes, const uint8_t* sca
  * [out_features, in_features / 2], w_scales [out_features, in_features / 32], as
  * lora_mx_quantize writes them (a scale byte above 252 may overflow); y [rows,
  * out_features] of `type`, written, one rounding of the tensor cores' fp32 sum.
- * in_features % 32 == 0, out_features % 8 == 0.  The linear delta goes on top:
- * lora_apply_linear(x, y, ...).
+ * in_features % 32 == 0, out_features % 8 == 0; at most 2^24 in_features, 2^30
+ * out_features (of all experts together), 2^28 rows and 2^30 tiles of 16 rows by 128
+ * features.  The linear delta goes on top: lora_apply_linear(x, y, ...).
  */
 LORA_API lora_status lora_mx_linear(const uint8_t* x_codes, const uint8_t* x_scales,
                                     const uint8_t* w_codes, const uint8_t* w_scales, void* y,
@@ -427,7 +429,7 @@ LORA_API lora_status lora_mx_expert_linear(const uint8_t* x_codes, const uint8_t
  * [T, features] (or NULL: 0; it may be out itself) and out [T, features] of
  * `type`; pair_row [T, top_k] as lora_group_experts writes it: -1 adds nothing,
  * anything else outside [0, rows_cap) neither (LORA_FLAG_BAD_ROW).
- * features % 8 == 0.
+ * features % 8 == 0, features <= 65535 * 1024, T <= 2^30.
  */
 LORA_API lora_status lora_combine_experts(const void* y_sorted, int32_t type,
                                           const int32_t* pair_row, const float* topk_weights,

@@ -257,3 +257,10 @@ def test_oracle_route_saturated_by_hand():
         assert O.route(x, bias, 3, "sigmoid")[0].tolist() == [[1, 0, 3]]
         assert O.route(x, bias, 3, "sigmoid", 2, 1)[0][0, :2].tolist() == [1, 0]
     assert O.route(x, [0.0, 0.0, 0.25, 0.0], 3, "sigmoid")[0].tolist() == [[0, 1, 3]]
+
+
+def test_combine_at_its_widest(lib):
+    """65535 blocks of 1024 columns are the grid's second dimension at its end."""
+    assert _combine(lib, T=0, F=65535 * 1024) == L.LORA_OK
+    for F in (65535 * 1024 + 8, 1 << 26):
+        assert _combine(lib, T=0, F=F) == L.LORA_ERR_UNSUPPORTED
