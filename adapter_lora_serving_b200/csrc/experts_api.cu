@@ -189,6 +189,11 @@ lora_status lora_group_experts(const int32_t* topk_ids, const int32_t* token_slo
                       {err_flags, "err_flags", 4, true}}));
   if ((token_slot == nullptr) != (row_slot == nullptr) && T > 0)
     return fail(LORA_ERR_INVALID, "%s: token_slot and row_slot go together", op);
+  // (pair_row holds the counts of many pairs until their rows are known)
+  const uintptr_t in = reinterpret_cast<uintptr_t>(topk_ids), bytes = (uintptr_t)T * top_k * 4;
+  const uintptr_t out = reinterpret_cast<uintptr_t>(pair_row);
+  if (in < out + bytes && out < in + bytes)
+    return fail(LORA_ERR_INVALID, "%s: pair_row overlaps topk_ids", op);
   lora::GroupParams p = {};
   p.ids = topk_ids; p.token_slot = token_slot; p.expert_offsets = expert_offsets;
   p.row_token = row_token; p.pair_row = pair_row; p.row_slot = row_slot; p.flags = err_flags;

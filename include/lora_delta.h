@@ -346,6 +346,7 @@ LORA_API lora_status lora_route_experts(const void* logits, int32_t type, const 
  * all int32.  topk_ids [T, top_k]: -1 takes no row, anything else outside [0,
  * num_experts) neither, and raises LORA_FLAG_BAD_EXPERT.  row_token and row_slot
  * beyond the N rows are left as they were.  token_slot [T]: any value, copied.
+ * pair_row must not overlap topk_ids.
  * num_experts <= LORA_ROUTE_MAX_EXPERTS, T * top_k <= 2^30.
  */
 LORA_API lora_status lora_group_experts(const int32_t* topk_ids, const int32_t* token_slot,

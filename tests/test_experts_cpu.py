@@ -264,3 +264,10 @@ def test_combine_at_its_widest(lib):
     assert _combine(lib, T=0, F=65535 * 1024) == L.LORA_OK
     for F in (65535 * 1024 + 8, 1 << 26):
         assert _combine(lib, T=0, F=F) == L.LORA_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("by", [0, 4, -4, 4092, -4092])
+def test_group_in_place_is_refused(lib, by):
+    """Many pairs keep their counts in pair_row while the ids are still read."""
+    assert _group(lib, ids=FAKE, pair=FAKE + by, T=512, k=2) == L.LORA_ERR_INVALID
+    assert "overlaps" in lib.lora_last_error().decode()
