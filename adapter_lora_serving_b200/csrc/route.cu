@@ -674,9 +674,25 @@ __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_k
 // Few experts (E <= EM <= 32), no groups, many tokens: a thread per token, its row in
 // registers.  The same keys and the same filter; the choices as five bits each.
 // 500000 tokens of 8 experts 12.8 us against 152.6 with a warp each, 262144 of 16 with
-// a bias 26.5 against 117.6; 8192 of 16 7.7 against 5.5.
-constexpr int kThreadTokens = 16384;   // tokens from which it is used
+// a bias 26.5 against 117.6.  A thread's time grows with its row and its choices and a
+// few tokens leave SMs idle, so it is used from 16384 tokens on and from
+// 16 EM E (top_k + 1) (us with a thread and with a warp each, sigmoid and a bias, the
+// slowest kind; softmax without one turns at half as many tokens):
+//   8 experts, 8 of them:  16384 tokens 10.3 and 10.4, 32768 10.7 and 18.4
+//   16, 4:    16384 9.4 and 8.7, 32768 10.4 and 15.5
+//   16, 12:   16384 18.7 and 12.0, 32768 19.5 and 21.8, 65536 23.7 and 40.0
+//   32, 1:    16384 10.3 and 7.8, 32768 12.7 and 13.4
+//   32, 4:    32768 18.5 and 15.5, 65536 29.2 and 28.5, 262144 83 and 114
+//   32, 8:    65536 41 and 33, 262144 122 and 130
+//   32, 12:   262144 165 and 149, 524288 311 and 293: a warp
+constexpr int kThreadTokens = 16384;
 constexpr int kThreadTopK = 12;       // 60 bits
+
+template <int EM>
+bool thread_per_token(const RouteParams& p) {   // EM: E rounded up to 8, 16 or 32
+  return p.E <= EM && p.num_groups == 1 && p.top_k <= (EM == 32 ? 8 : kThreadTopK) &&
+         p.T >= kThreadTokens && p.T >= 16 * EM * p.E * (p.top_k + 1);
+}
 
 template <int EM, typename V, typename Tol>
 LORA_DEV uint64_t choose_in_thread(int top_k, V (&key)[EM], Tol tol, int* count, bool* close) {
@@ -829,7 +845,10 @@ __global__ void __launch_bounds__(128) route_thread_kernel(const __grid_constant
 
 template <typename LT>
 cudaError_t route_typed(const RouteParams& p, cudaStream_t stream) {
-  if (p.E <= 32 && p.num_groups == 1 && p.top_k <= kThreadTopK && p.T >= kThreadTokens) {
+  const bool by_thread = p.E <= 8    ? thread_per_token<8>(p)
+                         : p.E <= 16 ? thread_per_token<16>(p)
+                                     : thread_per_token<32>(p);
+  if (by_thread) {
     const unsigned blocks = (unsigned)((p.T + 127LL) / 128);
     if (p.E <= 8) route_thread_kernel<8, LT><<<blocks, 128, 0, stream>>>(p);
     else if (p.E <= 16) route_thread_kernel<16, LT><<<blocks, 128, 0, stream>>>(p);

@@ -315,7 +315,8 @@ LORA_API lora_status lora_expert_apply(const void* x_sorted, void* y_sorted, con
  * one that 64 bits make (scores that saturate, underflow or vanish beside a bias),
  * goes to the lowest index.
  *   topk_weights[t, j] = s[t, id_j] (/ sum over the chosen, if renormalize) * scale
- * The bias takes part in the choice alone.  The weights are computed in fp32.
+ * The bias takes part in the choice alone.  The weights are computed in fp32 (the same
+ * for the same call; their last bits may change with T).
  * logits [T, num_experts] of `type`; bias [num_experts] fp32 or NULL; topk_ids
  * [T, top_k] int32; topk_weights [T, top_k] fp32.
  * An expert whose logit or bias is -inf is masked: it is never chosen (a masked

@@ -753,3 +753,29 @@ def test_route_many_tokens_close_and_masked_biases(name, score, E, k, kw):
     masked[0], masked[E - 2] = np.nan, np.inf
     _check_route(x, _dev(masked, t.float32), k, score=score, repeat=repeat, **kw)
     _check_route(x, _dev(np.full(E, -np.inf), t.float32), k, score=score, repeat=repeat, **kw)
+
+
+@pytest.mark.parametrize("name,score,E,k,rows,kw", [
+    ("bf16", "sigmoid", 32, 1, 8, dict()), ("f32", "softmax", 27, 2, 12, dict(renorm=False)),
+    ("f16", "sigmoid", 17, 4, 20, dict(scale=2.5)), ("f32", "softmax", 32, 8, 36, dict()),
+    ("bf16", "softmax", 16, 12, 13, dict(renorm=False)), ("bf16", "sigmoid", 9, 4, 5, dict()),
+    ("bf16", "softmax", 32, 9, 40, dict()), ("f32", "sigmoid", 8, 8, 4, dict())])
+def test_route_on_both_sides_of_a_thread_a_token(name, score, E, k, rows, kw):
+    """The number of tokens from which a thread takes a token grows with the row and
+    the choices: the same tokens few and `rows` times over, with close and masked
+    biases."""
+    t = _torch()
+    rng = np.random.default_rng(E * k + rows)
+    x = rng.standard_normal((4203, E)) * 2
+    x[7, :], x[8, 1:], x[9, 0] = -np.inf, -np.inf, np.nan
+    x[100:200] = np.round(x[100:200])
+    x = _dev(x, _dtype(name))
+    row = _host(x)[500]
+    e = np.exp(row - row.max())
+    s = 1 / (1 + np.exp(-row)) if score == "sigmoid" else e / e.sum()
+    close = 0.5 - s
+    masked = np.where(np.arange(E) % 5 == 2, -np.inf, 0.1 * rng.standard_normal(E))
+    for bias in (None, close, masked):
+        for repeat in (1, rows):
+            _check_route(x, None if bias is None else _dev(bias, t.float32), k, score=score,
+                         repeat=repeat, **kw)
