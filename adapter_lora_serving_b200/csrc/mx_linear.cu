@@ -1359,9 +1359,12 @@ Shape choose(const MxLinearParams& q, int dev, int sms) {
     while (s > 1 && clusters_at_once(dev, s) < tiles) --s;
     return max(1, s);
   };
-  // (with few k a tile's epilogue weighs more, and wider tiles are fewer: 512 x 8 rows
-  // of 128 experts, 768 by 2048: 33.9 us with 64 rows a tile, 40.2 with 32)
-  const long long fit = q.K <= 1024 && experts > 1 ? 2 * mean : mean;
+  // (with few k a tile's epilogue weighs more, and experts have ragged numbers of rows:
+  // a tile that holds half as many rows again as the mean, 8 to 128 experts of 256 to
+  // 1024 by 1024 to 4096.  128 of 768 by 4096, a mean of 14, 30 and 60 rows: 40, 45 and
+  // 50 us, 56, 58 and 65 by the mean; 8 of 512 by 4096, a mean of 20 and 40: 6.6 and
+  // 7.3, 7.7 and 8.7 by twice the mean)
+  const long long fit = q.K <= 1024 && experts > 1 ? mean + mean / 2 : mean;
   Shape best = {fit <= 16 ? 16 : fit <= 32 ? 32 : fit <= 64 ? 64 : 128, 1};
   best.splits = splits_for(tile_bound(q, best.rows));
   if (mean <= 128 || q.K % 128 != 0) return best;   // (256 rows: no room for unaligned scales)
