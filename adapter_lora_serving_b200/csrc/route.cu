@@ -170,6 +170,15 @@ LORA_DEV V scores(const RouteParams& p, const float (&x)[VPL], V (&s)[VPL]) {
   return inv;   // the largest: exp(0) / sum
 }
 
+// What a chosen expert's weight is a share of: softmax relative to the logit `top`, or
+// the sigmoid, to be renormalised relative to that of a negative `top`, the largest
+// chosen (so that nothing underflows to 0 / 0).
+LORA_DEV float weight_of(const RouteParams& p, float x, float top) {
+  if (p.score == LORA_SCORE_SOFTMAX) return expf(x - top);
+  if (x >= 0.0f || !p.renormalize) return 1.0f / (1.0f + expf(-x));
+  return expf(x - fminf(top, 0.0f)) / (1.0f + expf(x));
+}
+
 // Selection keys s + bias of the lane's experts; a masked logit has key 0, a masked
 // bias the key of -inf.
 template <int VPL, typename V>
@@ -632,16 +641,9 @@ __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_k
     const float xs = live ? to_f32(row[id]) : -INFINITY;
     float w;
     if (p.renormalize) {
-      // relative to the largest chosen score, so that nothing underflows to 0 / 0
       const uint32_t mu = warp_max(order_of(xs));
       const float top = is_open(mu) ? value_of(mu) : 0.0f;
-      if (p.score == LORA_SCORE_SOFTMAX) {
-        w = live ? expf(xs - top) : 0.0f;
-      } else {
-        const float m = fminf(top, 0.0f);
-        w = !live ? 0.0f
-                  : xs >= 0.0f ? 1.0f / (1.0f + expf(-xs)) : expf(xs - m) / (1.0f + expf(xs));
-      }
+      w = live ? weight_of(p, xs, top) : 0.0f;
       float sum = w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -657,9 +659,9 @@ __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_k
       for (int i = 0; i < VPL; ++i) sum += expf(x[i] - m);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      w = live ? expf(xs - m) / sum : 0.0f;
+      w = live ? weight_of(p, xs, m) / sum : 0.0f;
     } else {
-      w = live ? 1.0f / (1.0f + expf(-xs)) : 0.0f;
+      w = live ? weight_of(p, xs, 0.0f) : 0.0f;
     }
     if (lane < p.top_k) {
       const size_t o = (size_t)t * p.top_k + lane;
@@ -812,7 +814,6 @@ __global__ void __launch_bounds__(128) route_thread_kernel(const __grid_constant
       for (int i = 0; i < EM; ++i) key[i] = x[i];
       picks = choose_in_thread<EM, float>(p.top_k, key, Exact(), &count, &close);
     }
-    // weights, as in weight_of
     float top = -INFINITY, sum = 0.0f;
     if (p.renormalize) {
       for (int j = 0; j < count; ++j) top = fmaxf(top, to_f32(row[(picks >> (5 * j)) & 31]));
@@ -822,21 +823,15 @@ __global__ void __launch_bounds__(128) route_thread_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < EM; ++i) sum += expf(x[i] - top);
     }
-    const float m = fminf(top, 0.0f);
-    auto weight = [&](float xs) {
-      if (p.score == LORA_SCORE_SOFTMAX) return expf(xs - top);
-      if (xs >= 0.0f || !p.renormalize) return 1.0f / (1.0f + expf(-xs));
-      return expf(xs - m) / (1.0f + expf(xs));
-    };
     if (p.renormalize)
-      for (int j = 0; j < count; ++j) sum += weight(to_f32(row[(picks >> (5 * j)) & 31]));
+      for (int j = 0; j < count; ++j) sum += weight_of(p, to_f32(row[(picks >> (5 * j)) & 31]), top);
     else if (p.score == LORA_SCORE_SIGMOID)
       sum = 1.0f;
     const size_t o = (size_t)t * p.top_k;
     for (int j = 0; j < p.top_k; ++j) {
       const int id = j < count ? (int)((picks >> (5 * j)) & 31) : -1;
       p.ids[o + j] = id;
-      p.weights[o + j] = id >= 0 ? weight(to_f32(row[id])) / sum * p.scale : 0.0f;
+      p.weights[o + j] = id >= 0 ? weight_of(p, to_f32(row[id]), top) / sum * p.scale : 0.0f;
     }
   }
   if (p.flags != nullptr && __any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0)
