@@ -123,10 +123,12 @@ LORA_DEV void load_bias(const RouteParams& p, int lane, float (&bias)[VPL], bool
 }
 
 // Whether all experts have one bias, a finite one (VPL of them in each lane, e0 the
-// lane's first; the caller votes): then the order of the keys is that of the logits,
-// also where scores are equal in 64 bits.
+// lane's first; the caller votes), and no sum of two scores counts: then the order of
+// the keys is that of the logits, also where scores are equal in 64 bits.  Asked only
+// where keys are close.
 template <int VPL>
 LORA_DEV bool one_bias(const RouteParams& p, const float (&bias)[VPL], int e0) {
+  if (p.bias == nullptr || (p.num_groups > 1 && p.group_score == LORA_GROUP_TOP_PAIR)) return false;
   const float first = __ldg(p.bias);
   bool same = fabsf(first) < INFINITY;
 #pragma unroll
@@ -581,31 +583,37 @@ __device__ __noinline__ int select_in_double(const RouteParams& p, const LT* row
   load_row<VPL, LT>(row, lane, p.E, x);
   const bool finite = mask_row<VPL>(x, lane * VPL >= p.E, &bad);
   load_bias<VPL>(p, lane, bias, &bad);
-  scores<VPL, double>(p, x, s);
+  if (__all_sync(0xffffffffu, one_bias<VPL>(p, bias, lane * VPL))) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      s[i] = (double)x[i];
+      bias[i] = 0.0f;
+    }
+  } else {
+    scores<VPL, double>(p, x, s);
+  }
   return select_by_score<VPL, double, kBeside>(p, lane, group_span<VPL>(p), x, s, bias, finite,
                                                Exact(), &close, NoKey());
 }
 
-// One warp per token.  Without a bias, or with one for all (and without pair scores of
-// groups), the order of the scores is the order of the logits, so the logits
-// themselves are the keys and the choice is exact.  Else the keys are fp32 scores plus
-// bias; where two that decide the outcome lie within their error bound they are
-// compared in 64 bits (the filter), so that the chosen experts are those of keys in
-// 64 bits.  Bound by its instructions (about 950 a token with groups and a bias;
+// One warp per token.  Without a bias (and without pair scores of groups) the order
+// of the scores is the order of the logits, so the logits themselves are the keys and
+// the choice is exact.  Else the keys are fp32 scores plus bias; where two that decide
+// the outcome lie within their error bound they are compared in 64 bits (the filter),
+// or by their logits where all have one bias, so that the chosen experts are those of
+// keys in 64 bits.  Bound by its instructions (about 950 a token with groups and a bias;
 // 16384 tokens of 256 experts: 23.5 us, of which the rounds 6, the groups 5 and the
 // close calls 1.3; without groups and bias, 2048 of 128: 2.7 us).
 template <int VPL, typename LT>
 __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_kernel(const __grid_constant__ RouteParams p) {
   const int lane = threadIdx.x & 31;
   const int warps = (int)(blockDim.x >> 5);
-  bool by_score = p.bias != nullptr || (p.num_groups > 1 && p.group_score == LORA_GROUP_TOP_PAIR);
+  const bool by_score =
+      p.bias != nullptr || (p.num_groups > 1 && p.group_score == LORA_GROUP_TOP_PAIR);
   const int span = group_span<VPL>(p);
   bool bad = false;
   float bias[VPL];
   if (by_score) load_bias<VPL>(p, lane, bias, &bad);
-  if (p.bias != nullptr && (p.num_groups == 1 || p.group_score == LORA_GROUP_MAX) &&
-      __all_sync(0xffffffffu, one_bias<VPL>(p, bias, lane * VPL)))
-    by_score = false;
   for (long long t = (long long)blockIdx.x * warps + (threadIdx.x >> 5); t < p.T;
        t += (long long)gridDim.x * warps) {
     const LT* row = reinterpret_cast<const LT*>(p.logits) + (size_t)t * p.E;
@@ -619,6 +627,8 @@ __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_k
       const float smax = scores<VPL, float>(p, x, s);
       id = select_by_score<VPL, float, kLow>(p, lane, span, x, s, bias, finite,
                                              key_error<VPL>(p, smax), &close, [&](int e) {
+                                               if (__all_sync(0xffffffffu, one_bias<VPL>(p, bias, lane * VPL)))
+                                                 return e >= 0 ? (double)to_f32(row[e]) : 0.0;
                                                return exact_key<VPL, LT>(p, row, lane, e);
                                              });
       if (close) id = select_in_double<VPL, LT>(p, row, lane);
