@@ -140,8 +140,8 @@ class MoeLayer:
             L._refuse(op, f"x has {x.numel() // T} features a token, the layer {self.hidden}")
         for name, t, n in (("gate_logits", gate_logits, E), ("out", out, self.hidden),
                            ("residual", residual, self.hidden)):
-            if t is not None and t.__class__ is not int and t.dim() > 1 and t.shape[-1] != n:
-                L._refuse(op, f"{name} has rows of {t.shape[-1]}, not of {n}")
+            if t is not None and t.__class__ is not int and t.dim() == 2 and t.shape[1] != n:
+                L._refuse(op, f"{name} has rows of {t.shape[1]}, not of {n}")
         bf16, i32, rt = L.LORA_TYPE_BF16, "int32", self.router_adapters
         of_logits = bf16
         if rt is None:   # the routing takes logits of any LORA_TYPE_*

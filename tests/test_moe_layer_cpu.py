@@ -149,3 +149,20 @@ def test_adapters_are_checked_once():
         with pytest.raises(ValueError, match="adapters"):
             _layer(**bad)
     _layer()
+
+
+@pytest.mark.parametrize("router", [False, True])
+def test_other_shapes_of_the_same_rows_pass(router, monkeypatch):
+    """Logits by expert group, flat buffers, buffers with room for more tokens."""
+    import torch
+    bf16 = torch.bfloat16
+    monkeypatch.setattr(L, "_pointers", _types_only)
+    for kw in (dict(gate_logits=torch.zeros(T, 2, E // 2, dtype=bf16)),
+               dict(gate_logits=torch.zeros(T * E, dtype=bf16)),
+               dict(gate_logits=torch.zeros(T + 3, E, dtype=bf16)),
+               dict(out=torch.zeros(T + 1, HIDDEN, dtype=bf16)),
+               dict(x=torch.zeros(T, 4, HIDDEN // 4, dtype=bf16)),
+               dict(residual=torch.zeros(T, HIDDEN, dtype=bf16))):
+        with pytest.raises(Exception) as e:
+            _call(_layer(router=router), monkeypatch, **kw)
+        assert not isinstance(e.value, L.LoraError)
