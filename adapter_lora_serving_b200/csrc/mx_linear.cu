@@ -24,15 +24,15 @@
 // precomputed words.
 //
 // What bounds it.  Few rows: the weight's bytes (32 tokens x 8 of 128 experts, 2048
-// by 1536: 174 MB in 32 us, 5.2 TB/s with start and end; one row of 4096 by 28672:
-// 15.0 us, 9.6 being its 62.5 MB at the copy rate).  Where there are fewer tiles
+// by 1536: 166 MB in 31.2 us, 5.3 TB/s with start and end; one row of 4096 by 28672:
+// 14.7 us, 9.6 being its 62.5 MB at the copy rate).  Where there are fewer tiles
 // than SMs a cluster of `splits` CTAs shares a tile, each over its part of k, and
 // the partial sums are added through distributed shared memory in rank order (the
 // result does not depend on timing): 128 rows of 14336 by 4096 take 13.4 us instead
 // of 18.4.  Many rows: a 128 x 256 tile of one CTA is bound by shared memory (12 KB
 // read and 12 written per MMA of 135 cycles); two CTAs on one tile of 256 x 256
-// (below) take 8 and 8: 8192 rows of 4096 by 28672 in 356 us (5.4 PFLOP/s; 408 with
-// one CTA a tile), or 415 us where it runs long enough to meet the power limit.
+// (below) take 8 and 8: 8192 rows of 4096 by 28672 in 358 us (5.4 PFLOP/s; 408 with
+// one CTA a tile), or 421 us where it runs long enough to meet the power limit.
 //
 // Every wait is bounded; on a timeout the CTA raises LORA_FLAG_TIMEOUT, stops
 // issuing, lets its copies land, frees its tensor memory and exits.

@@ -601,9 +601,11 @@ __device__ __noinline__ int select_in_double(const RouteParams& p, const LT* row
 // the choice is exact.  Else the keys are fp32 scores plus bias; where two that decide
 // the outcome lie within their error bound they are compared in 64 bits (the filter),
 // or by their logits where all have one bias, so that the chosen experts are those of
-// keys in 64 bits.  Bound by its instructions (about 950 a token with groups and a bias;
-// 16384 tokens of 256 experts: 23.5 us, of which the rounds 6, the groups 5 and the
-// close calls 1.3; without groups and bias, 2048 of 128: 2.7 us).
+// keys in 64 bits.  Bound by its instructions (about 950 a token with groups and a bias,
+// 48 of them loads and stores of spilled registers: the 64-bit calls within the loop
+// keep a token's state across them; issued in 69 % of the cycles; 16384 tokens of 256
+// experts: 23.2 us, of which the rounds 6, the groups 5 and the close calls 1.3;
+// without groups and bias, 2048 of 128: 2.7 us).
 template <int VPL, typename LT>
 __global__ void __launch_bounds__(256, VPL <= 8 ? 4 : VPL <= 16 ? 3 : 2) route_kernel(const __grid_constant__ RouteParams p) {
   const int lane = threadIdx.x & 31;
