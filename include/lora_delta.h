@@ -310,10 +310,10 @@ LORA_API lora_status lora_expert_apply(const void* x_sorted, void* y_sorted, con
  * only those of the best top_groups groups (by group_score of their keys) can be
  * chosen.  topk_ids[t] are the top_k experts of the largest keys, in descending
  * order.  Without a bias, or with one that is the same finite number for all experts,
- * and without LORA_GROUP_TOP_PAIR the logits themselves are compared (the scores have
- * their order); else keys, and sums of two, as computed in 64 bits.  Every tie, also
- * one that 64 bits make (scores that saturate, underflow or vanish beside a bias),
- * goes to the lowest index.
+ * the logits themselves are compared (the scores have their order), unless groups are
+ * left out (top_groups < num_groups) by LORA_GROUP_TOP_PAIR; else keys, and sums of
+ * two, as computed in 64 bits.  Every tie, also one that 64 bits make (scores that
+ * saturate, underflow or vanish beside a bias), goes to the lowest index.
  *   topk_weights[t, j] = s[t, id_j] (/ sum over the chosen, if renormalize) * scale
  * The bias takes part in the choice alone.  The weights are computed in fp32 (the same
  * for the same call; their last bits may change with T).

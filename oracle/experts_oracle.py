@@ -38,7 +38,8 @@ def route(logits, bias, top_k, score="softmax", num_groups=1, top_groups=1, pair
         # without a bias, or with one for all, the order of the scores is that of the
         # logits, also where scores underflow or saturate
         one = bias is None or (np.isfinite(b).all() and (b == b[0]).all())
-        by_logit = one and not (num_groups > 1 and pair)
+        # (sums of two scores count where groups are left out by them)
+        by_logit = one and not (top_groups < num_groups and pair)
         key = np.where(open_, x if by_logit else s + np.where(open_, b, 0.0), -np.inf)
         if num_groups > 1 and top_groups < num_groups:
             n = E // num_groups

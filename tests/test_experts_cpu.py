@@ -271,3 +271,10 @@ def test_group_in_place_is_refused(lib, by):
     """Many pairs keep their counts in pair_row while the ids are still read."""
     assert _group(lib, ids=FAKE, pair=FAKE + by, T=512, k=2) == L.LORA_ERR_INVALID
     assert "overlaps" in lib.lora_last_error().decode()
+
+
+def test_oracle_route_with_every_group_kept_by_hand():
+    """Sums of two scores decide nothing when no group is left out."""
+    x = [[50.0, 60.0, 0.0, 50.0]]
+    for bias in (None, [1.0] * 4):
+        assert O.route(x, bias, 3, "sigmoid", 2, 2, True)[0].tolist() == [[1, 0, 3]]

@@ -779,3 +779,16 @@ def test_route_on_both_sides_of_a_thread_a_token(name, score, E, k, rows, kw):
         for repeat in (1, rows):
             _check_route(x, None if bias is None else _dev(bias, t.float32), k, score=score,
                          repeat=repeat, **kw)
+
+
+@pytest.mark.parametrize("E", [64, 96, 512])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_with_every_group_kept(E, score):
+    """The choice is that without groups, also among scores equal in 64 bits."""
+    rng = np.random.default_rng(E)
+    x = np.round(rng.uniform(-900, 900, (20, E))) * (1.0 if score == "softmax" else 0.25)
+    for bias in (None, np.full(E, 0.5), 0.1 * rng.standard_normal(E)):
+        want = _ids(x, bias, 8, score=score)
+        for pair in (False, True):
+            assert (_ids(x, bias, 8, score=score, G=8, g=8, pair=pair) == want).all()
+    _check_route(_dev(x, _dtype("f32")), None, 8, score=score, G=8, g=8, pair=True)
